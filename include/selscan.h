@@ -65,7 +65,8 @@ typedef enum {
     SS_ERR_CUDA = 6,               /* the CUDA runtime reported an error */
     SS_ERR_BAD_CONFIG = 7,         /* ss_fwd_with_config: unsupported launch shape */
     SS_ERR_WORKSPACE = 8,          /* the launch shape needs a larger workspace */
-    SS_ERR_SCRATCH_LIMIT = 9       /* ss_fwd_noalloc: needs more than SS_NOALLOC_SCRATCH_BYTES */
+    SS_ERR_SCRATCH_LIMIT = 9,      /* ss_fwd_noalloc: needs more than SS_NOALLOC_SCRATCH_BYTES */
+    SS_ERR_OVERLAP = 10            /* two buffers that must be distinct are the same */
 } ss_status;
 
 typedef enum { SS_F32 = 0, SS_BF16 = 1 } ss_dtype;
@@ -487,6 +488,153 @@ ss_status ss_fwd_hostio_streams(const ss_desc *desc, const void *h_u, const void
                                 void *d_y, float *d_last_state, void *d_workspace,
                                 size_t workspace_bytes, const ss_stream_t *streams, int nstreams,
                                 int chunks);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Operators around the scan.  A layer normalises its input, convolves it along
+ * the sequence and runs the scan (or a plain gated recurrence) over the
+ * result; the entries below are those steps on the scan's own (batch, dim, L)
+ * tensors, with its descriptor (dstate is not read), types, sequence starts,
+ * states and errors.  Arithmetic, sums, statistics and the recurrence's state
+ * are float32; results are rounded once, to the output's type, and are
+ * bitwise reproducible.  Buffers may not overlap unless an entry says so.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Normalisation over the channels, for every batch entry b and step l: layer
+ * norm (rms == 0), or its form without the mean (rms != 0), the RMSNorm of
+ * the mamba-minimal block (Mamba-minimal项目解析, 核心组件解析: ResidualBlock
+ * normalises before the mixer):
+ *   m = mean_d x[b,d,l] (0 with rms),  r = (mean_d (x - m)^2 + eps)^(-1/2)
+ *   y[b,d,l] = (x[b,d,l] - m) r weight[d] + bias[d]
+ * With L = 1, x is batch rows of dim contiguous elements (the residual stream
+ * of a model, one row per token).
+ *   x       device, (B, D, L) in_dtype
+ *   weight, bias  device, (D,) float32, or NULL (1, 0)
+ *   y       device, (B, D, L) out_dtype
+ *   mean, rstd  device, (B, L) float32 outputs, or NULL: m and r, for
+ *           ss_norm_bwd (mean is not written with rms)
+ * An empty tensor launches nothing.  SS_ERR_BAD_SHAPE for dim >= 2^31, more
+ * than 2^31 rows (L = 1) or 2^32 steps (batch * L).
+ */
+ss_status ss_norm_fwd(const ss_desc *desc, const void *x, const float *weight, const float *bias, float eps, int rms,
+                      void *y, float *mean, float *rstd, ss_stream_t stream);
+
+/*
+ * Backward of ss_norm_fwd: with xh = (x - mean) rstd and v = dy weight,
+ *   dx = rstd (v - mean_d v - xh mean_d(v xh))   (rms: without the second term)
+ *   dweight[d] = sum_(b,l) dy xh,  dbias[d] = sum_(b,l) dy
+ *   mean      device, (B, L) float32 as the forward wrote it; NULL: the rms form
+ *   rstd      device, (B, L) float32
+ *   dy        device, (B, D, L) out_dtype
+ *   dx        device, (B, D, L) in_dtype
+ *   dweight, dbias  device, (D,) float32 outputs, or NULL: not computed
+ *   workspace device, 16-byte aligned, ss_norm_bwd_workspace_bytes(desc) bytes
+ *             when dweight or dbias is given; scratch, not shared by calls
+ *             that overlap on the GPU
+ * With no steps dweight and dbias are zero.
+ */
+ss_status ss_norm_bwd(const ss_desc *desc, const void *x, const float *weight, const float *mean, const float *rstd,
+                      const void *dy, void *dx, float *dweight, float *dbias, void *workspace, size_t workspace_bytes,
+                      ss_stream_t stream);
+
+/* Bytes of workspace ss_norm_bwd needs for `desc` (0 for an invalid or empty descriptor). */
+size_t ss_norm_bwd_workspace_bytes(const ss_desc *desc);
+
+/*
+ * Causal depthwise convolution along the sequence (the conv1d between in_proj
+ * and the scan; 告别‘炼丹’ §1.1, d_conv = 4), width W in 2..8:
+ *   p[b,d,t] = bias[d] + sum_(j < W) weight[d,j] x[b,d,t-(W-1)+j]
+ *   y = p, or p sigmoid(p) (silu != 0)
+ *   x       device, (B, D, L) in_dtype
+ *   weight  device, (D, W) float32;  bias (D,) float32 or NULL
+ *   initial_state  device, (B, D, W-1) in_dtype: the inputs before step 0,
+ *           oldest first, or NULL (zeros)
+ *   reset   device, (B, L) bytes, or NULL: nonzero where a new sequence
+ *           starts (as ss_fwd_reset): no output at or after a start takes an
+ *           input from before it
+ *   y       device, (B, D, L) out_dtype
+ *   last_state  device, (B, D, W-1) in_dtype output, or NULL: the last W-1
+ *           inputs of each row (those before step 0 come from the initial
+ *           state, those before the last start are zero): the initial state
+ *           of the next piece
+ * x is read where its neighbours' outputs are written, so y == x, and
+ * last_state == initial_state (L > 0), are refused with SS_ERR_OVERLAP.
+ * SS_ERR_BAD_SHAPE for another width.
+ */
+ss_status ss_conv_fwd(const ss_desc *desc, int width, const void *x, const float *weight, const float *bias, int silu,
+                      const void *initial_state, const uint8_t *reset, void *y, void *last_state, ss_stream_t stream);
+
+/*
+ * Backward of ss_conv_fwd: the gradients of sum(dy y) (plus
+ * sum(d_last_state last_state) when that is given).
+ *   dy            device, (B, D, L) out_dtype
+ *   d_last_state  device, (B, D, W-1) in_dtype, or NULL (zero)
+ *   dx            device, (B, D, L) in_dtype
+ *   dweight, dbias  device, (D, W) and (D,) float32 outputs, or NULL: not written
+ *   d_initial_state device, (B, D, W-1) in_dtype output, or NULL
+ * Other arguments as ss_conv_fwd.  Needs no workspace.
+ */
+ss_status ss_conv_bwd(const ss_desc *desc, int width, const void *x, const float *weight, const float *bias, int silu,
+                      const void *initial_state, const uint8_t *reset, const void *dy, const void *d_last_state,
+                      void *dx, float *dweight, float *dbias, void *d_initial_state, ss_stream_t stream);
+
+/*
+ * One decoding step of ss_conv_fwd (desc->seqlen must be 1, SS_ERR_BAD_SHAPE
+ * otherwise): x, y (B, D); state device, (B, D, W-1) in_dtype, read and then
+ * moved up by one input in place.
+ */
+ss_status ss_conv_step(const ss_desc *desc, int width, const void *x, const float *weight, const float *bias, int silu,
+                       void *state, void *y, ss_stream_t stream);
+
+/*
+ * Gated linear recurrence, one state per channel:
+ *   a[b,d,t] = g[b,d,t], or sigmoid(g[b,d,t])   (gate_sigmoid != 0)
+ *   h[b,d] <- a h[b,d] + x[b,d,t],  or  a h + (1 - a) x   (couple != 0)
+ *   y[b,d,t] = h[b,d], times silu(z[b,d,t]) when z is given
+ *   x, g, z  device, (B, D, L) in_dtype (z NULL: no output gate)
+ *   initial_state  device, (B, D) float32: the state before step 0, or NULL
+ *            (zero); may be the same buffer as last_state
+ *   reset    device, (B, L) bytes, or NULL: nonzero where a new sequence
+ *            starts (as ss_fwd_reset); nothing is carried into such a step,
+ *            whatever the state before it holds
+ *   y        device, (B, D, L) out_dtype, or NULL (only the state is wanted)
+ *   last_state  device, (B, D) float32 output, or NULL
+ *   ckpt     device, ss_glr_ckpt_elems(desc) float32 output, or NULL: states
+ *            along the rows for ss_glr_bwd
+ * With L = 0 the last state is the initial one.  SS_ERR_BAD_SHAPE for more
+ * than 2^31 rows (batch * dim).
+ */
+ss_status ss_glr_fwd(const ss_desc *desc, const void *x, const void *g, const void *z, int gate_sigmoid, int couple,
+                     const float *initial_state, const uint8_t *reset, void *y, float *last_state, float *ckpt,
+                     ss_stream_t stream);
+
+/* Floats in the checkpoints of a forward of `desc`: one state per 256 steps of
+ * a row (0 for an invalid or empty descriptor).  Their layout is the library's. */
+size_t ss_glr_ckpt_elems(const ss_desc *desc);
+
+/*
+ * Backward of ss_glr_fwd from its checkpoints (of the same x, g, initial
+ * state and starts): the gradients of sum(dy y), plus sum(d_last_state
+ * last_state) when that is given.
+ *   dy         device, (B, D, L) out_dtype
+ *   d_last_state  device, (B, D) float32, or NULL (zero)
+ *   dx, dg, dz device, (B, D, L) in_dtype; dz required exactly when z is given
+ *   d_initial_state  device, (B, D) float32 output, or NULL; may be the same
+ *              buffer as d_last_state
+ * Needs no workspace.
+ */
+ss_status ss_glr_bwd(const ss_desc *desc, const void *x, const void *g, const void *z, int gate_sigmoid, int couple,
+                     const uint8_t *reset, const float *ckpt, const void *dy, const float *d_last_state, void *dx,
+                     void *dg, void *dz, float *d_initial_state, ss_stream_t stream);
+
+/*
+ * One decoding step of ss_glr_fwd (desc->seqlen must be 1, SS_ERR_BAD_SHAPE
+ * otherwise): x, g, z, y (B, D); state (B, D) float32, updated in place.
+ */
+ss_status ss_glr_step(const ss_desc *desc, const void *x, const void *g, const void *z, int gate_sigmoid, int couple,
+                      float *state, void *y, ss_stream_t stream);
 
 /* Static description of a status code (never NULL). */
 const char *ss_status_string(ss_status status);

@@ -52,6 +52,13 @@ def _compile_jobs(verbose: bool):
                      os.path.join(BUILD_DIR, "selscan.o")], "selscan"),
             (base + [os.path.join(CSRC, "ss_noalloc.cu"), "-o",
                      os.path.join(BUILD_DIR, "ss_noalloc.o")], "ss_noalloc")]
+    # the operators around the scan
+    for name in ("ss_norm", "ss_conv", "ss_glr"):
+        jobs.append((base + [os.path.join(CSRC, name + ".cu"), "-o", os.path.join(BUILD_DIR, name + ".o")], name))
+    for tin, tout, tag in DTYPE_PAIRS:
+        name = f"conv_{tag}"
+        jobs.append((base + [f"-DSS_INST_TIN={tin}", f"-DSS_INST_TOUT={tout}", f"-DSS_INST_NAME={tag}",
+                             os.path.join(CSRC, "ss_conv_inst.cu"), "-o", os.path.join(BUILD_DIR, name + ".o")], name))
     for tin, tout, tag in DTYPE_PAIRS:
         for n in BWD_STATE_BUCKETS:
             name = f"bwd_{tag}_n{n}"

@@ -1094,6 +1094,7 @@ const char *ss_status_string(ss_status status) {
         case SS_ERR_BAD_CONFIG: return "unsupported launch shape";
         case SS_ERR_WORKSPACE: return "workspace missing or too small";
         case SS_ERR_SCRATCH_LIMIT: return "needs more scratch than the no-alloc entry's static array";
+        case SS_ERR_OVERLAP: return "two buffers that must be distinct are the same";
     }
     return "unknown status";
 }

@@ -1,0 +1,68 @@
+// The convolution's kernels for one type pair: compiled once per
+// (SS_INST_TIN, SS_INST_TOUT) with SS_INST_NAME as the launchers' suffix.
+#include "ss_conv.cuh"
+
+#if !defined(SS_INST_TIN) || !defined(SS_INST_TOUT) || !defined(SS_INST_NAME)
+#error "compile with -DSS_INST_TIN=... -DSS_INST_TOUT=... -DSS_INST_NAME=..."
+#endif
+
+#define SS_CAT2(A, B) A##_##B
+#define SS_CAT(A, B) SS_CAT2(A, B)
+
+namespace selscan {
+namespace {
+
+using Tin = SS_INST_TIN;
+using Tout = SS_INST_TOUT;
+
+template <int W>
+cudaError_t fwd(cudaStream_t s, ConvParams &p) {
+    const int64_t n = p.batch * p.dim * p.L;
+    p.main_blocks = (n + kV * 256 - 1) / (kV * 256);
+    const int64_t tail = p.last ? (p.batch * p.dim * (W - 1) + 255) / 256 : 0;
+    if (p.main_blocks + tail > INT_MAX) return cudaErrorInvalidValue;
+    const unsigned grid = (unsigned)(p.main_blocks + tail);
+    if (p.reset) conv_fwd_kernel<Tin, Tout, W, true><<<grid, 256, 0, s>>>(p);
+    else conv_fwd_kernel<Tin, Tout, W, false><<<grid, 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <int W>
+cudaError_t bwd(cudaStream_t s, const ConvParams &p) {
+    // Blocks per channel: enough for about eight blocks per SM, no more than
+    // the channel's vectors feed.
+    const int64_t vecs = p.batch * ((p.L + 2 * kV - 2) / kV);
+    int nblk = 1;
+    while (nblk < 8 && p.dim * nblk < (int64_t)layer_sm_count() * 8 && vecs > (int64_t)nblk * kConvBwdThreads) nblk *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(p.dim * nblk));
+    cfg.blockDim = dim3(kConvBwdThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)nblk;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return p.reset ? cudaLaunchKernelEx(&cfg, conv_bwd_kernel<Tin, Tout, W, true>, p, nblk)
+                   : cudaLaunchKernelEx(&cfg, conv_bwd_kernel<Tin, Tout, W, false>, p, nblk);
+}
+
+}  // namespace
+
+#define SS_WIDTHS(F)                    \
+    switch (width) {                    \
+        case 2: return F<2>(s, p);      \
+        case 3: return F<3>(s, p);      \
+        case 4: return F<4>(s, p);      \
+        case 5: return F<5>(s, p);      \
+        case 6: return F<6>(s, p);      \
+        case 7: return F<7>(s, p);      \
+        case 8: return F<8>(s, p);      \
+        default: return cudaErrorInvalidValue; \
+    }
+
+cudaError_t SS_CAT(conv_fwd, SS_INST_NAME)(int width, cudaStream_t s, ConvParams &p) { SS_WIDTHS(fwd) }
+cudaError_t SS_CAT(conv_bwd, SS_INST_NAME)(int width, cudaStream_t s, const ConvParams &p) { SS_WIDTHS(bwd) }
+
+}  // namespace selscan

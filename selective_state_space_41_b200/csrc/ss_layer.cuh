@@ -1,0 +1,200 @@
+// What the operators around the scan (normalisation, causal convolution,
+// gated recurrence) share: eight-element vectors of a (batch, dim, L) tensor,
+// the logistic function with its complement, masks of sequence starts, and
+// the host-side checks of a descriptor.
+//
+// Rows of L steps start at multiples of L elements, so with an odd length no
+// row but the first starts on a 16-byte boundary.  The kernels that walk rows
+// therefore count "virtual" steps from the 8-element boundary at or before
+// the row's start: every vector is then aligned, the first and the last one
+// of a row hold a few elements of the neighbouring rows, and those are
+// masked.  All tensors of a call have the same shape, so one shift serves all.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <climits>
+#include <cstdint>
+#include <initializer_list>
+
+#include "selscan.h"
+#include "ss_fwd_kernel.cuh"
+
+namespace selscan {
+
+constexpr int kV = 8;  // elements per vector: 16 bytes of bf16, 32 of fp32
+
+// Eight elements as they lie in memory.
+template <typename T>
+struct Vec8 {
+    static constexpr int kWords = kV * sizeof(T) / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ float operator[](int i) const { return Io<T>::widen(w, i); }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) w[k] = 0u;
+    }
+    // The vector at an element index that is a multiple of 8 (16-byte aligned).
+    __device__ __forceinline__ void load(const T *p, int64_t e) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(p + e);
+#pragma unroll
+        for (int k = 0; k < kWords / 4; ++k) {
+            const uint4 u = __ldg(q + k);
+            w[4 * k] = u.x, w[4 * k + 1] = u.y, w[4 * k + 2] = u.z, w[4 * k + 3] = u.w;
+        }
+    }
+    __device__ __forceinline__ void set(const T *p, int64_t e, int i) {
+        const uint32_t b = Io<T>::bits(p, e);
+        if constexpr (sizeof(T) == 4) w[i] = b;
+        else w[i >> 1] |= b << (16 * (i & 1));
+    }
+    // Elements [lo, hi) of it; the others are zero.
+    __device__ __forceinline__ void load_part(const T *p, int64_t e, int lo, int hi) {
+        clear();
+#pragma unroll
+        for (int i = 0; i < kV; ++i)
+            if (i >= lo && i < hi) set(p, e + i, i);
+    }
+};
+
+// The vector at element e, of which [lo, hi) may be read.
+template <typename T>
+__device__ __forceinline__ void load8(Vec8<T> &r, const T *p, int64_t e, int lo, int hi, bool vec) {
+    if (vec && lo <= 0 && hi >= kV) r.load(p, e);
+    else r.load_part(p, e, lo, hi);
+}
+
+__device__ __forceinline__ float load_elem(const float *p, int64_t i) { return __ldg(p + i); }
+__device__ __forceinline__ float load_elem(const __nv_bfloat16 *p, int64_t i) {
+    return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short *>(p) + i) << 16);
+}
+
+__device__ __forceinline__ void put(float *p, int64_t i, float v) { p[i] = v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, int64_t i, float v) { p[i] = __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ void store_vec(float *p, const float (&v)[kV]) {
+    float4 *q = reinterpret_cast<float4 *>(p);
+    q[0] = make_float4(v[0], v[1], v[2], v[3]);
+    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const float (&v)[kV]) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// Elements [lo, hi) of v to the vector at element e.
+template <typename T>
+__device__ __forceinline__ void store8(T *p, int64_t e, int lo, int hi, bool vec, const float (&v)[kV]) {
+    if (vec && lo <= 0 && hi >= kV) {
+        store_vec(p + e, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kV; ++i)
+            if (i >= lo && i < hi) put(p, e + i, v[i]);
+    }
+}
+
+__device__ __forceinline__ int clamp8(int64_t v) { return v < 0 ? 0 : v > kV ? kV : (int)v; }
+
+// s = sigmoid(v) and c = 1 - s, both to full relative precision: with
+// e = exp(-|v|) in [0, 1], 1 / (1 + e) is the larger of the two and
+// e / (1 + e) the smaller, so nothing overflows and the smaller one does not
+// come from a subtraction.  kFast (bf16 inputs): exponential and reciprocal
+// on the SFU, some 1e-7 relative; otherwise expf and an IEEE division.
+template <bool kFast>
+__device__ __forceinline__ void sigmoid2(float v, float &s, float &c) {
+    float e, r;
+    if constexpr (kFast) {
+        e = sfu_exp2(-fabsf(v) * kLog2e);
+        r = sfu_rcp(1.f + e);
+    } else {
+        e = expf(-fabsf(v));
+        r = 1.f / (1.f + e);
+    }
+    const float q = e * r;
+    s = v >= 0.f ? r : q;
+    c = v >= 0.f ? q : r;
+}
+
+// Bit i: whether byte i of the pair of words is nonzero.
+__device__ __forceinline__ uint32_t nonzero_bytes(uint32_t lo, uint32_t hi) {
+    // one per nonzero byte, then the four ones gathered into bits 24..27 (the
+    // ten partial products below them fall on different bits: no carries)
+    const uint32_t a = (__vminu4(lo, 0x01010101u) * 0x01020408u) >> 24;
+    const uint32_t b = (__vminu4(hi, 0x01010101u) * 0x01020408u) >> 24;
+    return (a & 15u) | ((b & 15u) << 4);
+}
+
+// Bits lo..hi-1 of the start mask of eight steps from byte m of `reset`, whose
+// bytes [0, n) may be read.  Two aligned words where both lie inside, single
+// bytes at the mask's ends.
+__device__ __forceinline__ uint32_t start_bits(const uint8_t *reset, int64_t m, int64_t n, int lo, int hi) {
+    if (hi <= lo) return 0u;
+    const uint32_t keep = ((1u << hi) - 1u) & ~((1u << lo) - 1u);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(reset) + (uintptr_t)m;
+    const int off = (int)(at & 7);
+    if (m - off >= 0 && m - off + 16 <= n) {
+        const uint2 *q = reinterpret_cast<const uint2 *>(at - off);
+        const uint2 u = __ldg(q), v = __ldg(q + 1);
+        const unsigned long long a = ((unsigned long long)u.y << 32) | u.x, b = ((unsigned long long)v.y << 32) | v.x;
+        const unsigned long long x = off ? (a >> (8 * off)) | (b << (64 - 8 * off)) : a;
+        return nonzero_bytes((uint32_t)x, (uint32_t)(x >> 32)) & keep;
+    }
+    uint32_t bits = 0;
+    for (int i = lo; i < hi; ++i)
+        if (__ldg(reset + m + i)) bits |= 1u << i;
+    return bits;
+}
+
+// ------------------------------------------------------------------- host
+struct LayerSizes {
+    int64_t rows, elems;  // batch * dim, batch * dim * seqlen
+};
+
+// The descriptor's sizes and types, as the scan's entries check them, but
+// for dstate, which these operators do not read.
+inline ss_status check_layer(const ss_desc *desc, LayerSizes *s) {
+    if (!desc) return SS_ERR_NULL_POINTER;
+    if (desc->batch < 0 || desc->dim < 0 || desc->seqlen < 0) return SS_ERR_BAD_SHAPE;
+    const bool in_ok = desc->in_dtype == SS_F32 || desc->in_dtype == SS_BF16;
+    const bool out_ok = desc->out_dtype == desc->in_dtype || (desc->in_dtype == SS_BF16 && desc->out_dtype == SS_F32);
+    if (!in_ok || !out_ok) return SS_ERR_UNSUPPORTED_DTYPE;
+    constexpr int64_t kMost = INT64_MAX / 64;
+    const int64_t d = desc->dim > 0 ? desc->dim : 1, l = desc->seqlen > 0 ? desc->seqlen : 1;
+    const int64_t b = desc->batch > 0 ? desc->batch : 1;
+    if (d > kMost / b || l > kMost / (b * d)) return SS_ERR_BAD_SHAPE;
+    s->rows = desc->batch * desc->dim;
+    s->elems = s->rows * desc->seqlen;
+    return SS_OK;
+}
+
+inline size_t layer_size(ss_dtype t) { return t == SS_BF16 ? 2 : 4; }
+inline bool layer_aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+inline bool vec_ok(std::initializer_list<const void *> ps) {  // 16-byte vectors at every base (null: absent)
+    for (const void *q : ps)
+        if (!layer_aligned(q, 16)) return false;
+    return true;
+}
+inline ss_status status_of(cudaError_t e) { return e == cudaSuccess ? SS_OK : SS_ERR_CUDA; }
+
+// SMs of the current device (asked once per device).
+inline int layer_sm_count() {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int> cache[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 148;
+    int v = cache[dev].load(std::memory_order_relaxed);
+    if (v > 0) return v;
+    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) v = 148;
+    cache[dev].store(v, std::memory_order_relaxed);
+    return v;
+}
+
+}  // namespace selscan
+
+// KERNEL<Tin, Tout> for the descriptor's type pair, as a launch of `CALL`.
+#define SS_LAYER_DISPATCH(DESC, CALL)                                                     \
+    ((DESC)->in_dtype == SS_F32    ? CALL<float, float>                                   \
+     : (DESC)->out_dtype == SS_F32 ? CALL<__nv_bfloat16, float> : CALL<__nv_bfloat16, __nv_bfloat16>)

@@ -30,7 +30,7 @@ _DTYPE_CODE = {torch.float32: SS_F32, torch.bfloat16: SS_BF16}
 STATUS_NAMES = {0: "SS_OK", 1: "SS_ERR_NULL_POINTER", 2: "SS_ERR_BAD_SHAPE",
                 3: "SS_ERR_UNSUPPORTED_DTYPE", 4: "SS_ERR_UNSUPPORTED_DSTATE",
                 5: "SS_ERR_MISALIGNED", 6: "SS_ERR_CUDA", 7: "SS_ERR_BAD_CONFIG",
-                8: "SS_ERR_WORKSPACE", 9: "SS_ERR_SCRATCH_LIMIT"}
+                8: "SS_ERR_WORKSPACE", 9: "SS_ERR_SCRATCH_LIMIT", 10: "SS_ERR_OVERLAP"}
 
 # SS_NOALLOC_SCRATCH_BYTES: the static scratch array behind ss_fwd_noalloc.
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -40,7 +40,8 @@ EXPORTS = ("ss_fwd", "ss_fwd_ws", "ss_fwd_workspace_bytes", "ss_fwd_with_config"
            "ss_fwd_reset", "ss_fwd_heuristic", "ss_fwd_hostio", "ss_fwd_hostio_streams", "ss_fwd_noalloc",
            "ss_step", "ss_bwd", "ss_bwd_reset", "ss_bwd_state", "ss_bwd_workspace_bytes", "ss_status_string",
            "ss_version", "ss_device_status", "ss_fwd_dtproj", "ss_bwd_heuristic", "ss_fwd_ckpt", "ss_bwd_ckpt",
-           "ss_bwd_ckpt_workspace_bytes", "ss_fwd_xdbl")
+           "ss_bwd_ckpt_workspace_bytes", "ss_fwd_xdbl", "ss_norm_fwd", "ss_norm_bwd", "ss_norm_bwd_workspace_bytes",
+           "ss_conv_fwd", "ss_conv_bwd", "ss_conv_step", "ss_glr_fwd", "ss_glr_bwd", "ss_glr_step", "ss_glr_ckpt_elems")
 
 
 class SelscanError(RuntimeError):
@@ -117,6 +118,28 @@ def lib():
         L.ss_bwd_ckpt_workspace_bytes.argtypes = [DP]
         L.ss_bwd_heuristic.restype = I
         L.ss_bwd_heuristic.argtypes = [DP, ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(I)]
+        # the operators around the scan (layer_ops.py)
+        F = ctypes.c_float
+        L.ss_norm_fwd.restype = I
+        L.ss_norm_fwd.argtypes = [DP, P, P, P, F, I, P, P, P, P]
+        L.ss_norm_bwd.restype = I
+        L.ss_norm_bwd.argtypes = [DP] + [P] * 9 + [SZ, P]
+        L.ss_norm_bwd_workspace_bytes.restype = SZ
+        L.ss_norm_bwd_workspace_bytes.argtypes = [DP]
+        L.ss_conv_fwd.restype = I
+        L.ss_conv_fwd.argtypes = [DP, I, P, P, P, I, P, P, P, P, P]
+        L.ss_conv_bwd.restype = I
+        L.ss_conv_bwd.argtypes = [DP, I, P, P, P, I] + [P] * 9
+        L.ss_conv_step.restype = I
+        L.ss_conv_step.argtypes = [DP, I, P, P, P, I, P, P, P]
+        L.ss_glr_fwd.restype = I
+        L.ss_glr_fwd.argtypes = [DP, P, P, P, I, I] + [P] * 6
+        L.ss_glr_bwd.restype = I
+        L.ss_glr_bwd.argtypes = [DP, P, P, P, I, I] + [P] * 9
+        L.ss_glr_step.restype = I
+        L.ss_glr_step.argtypes = [DP, P, P, P, I, I, P, P, P]
+        L.ss_glr_ckpt_elems.restype = SZ
+        L.ss_glr_ckpt_elems.argtypes = [DP]
         L.ss_status_string.restype = ctypes.c_char_p
         L.ss_status_string.argtypes = [I]
         L.ss_version.restype = I
