@@ -35,6 +35,12 @@ struct Vec8 {
 #pragma unroll
         for (int k = 0; k < kWords; ++k) w[k] = 0u;
     }
+    // Makes the words opaque here: what was computed from them before is
+    // computed anew after it, rather than kept in registers meanwhile.
+    __device__ __forceinline__ void again() {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) asm volatile("" : "+r"(w[k]));
+    }
     // The vector at an element index that is a multiple of 8 (16-byte aligned).
     __device__ __forceinline__ void load(const T *p, int64_t e) {
         const uint4 *q = reinterpret_cast<const uint4 *>(p + e);
@@ -44,17 +50,21 @@ struct Vec8 {
             w[4 * k] = u.x, w[4 * k + 1] = u.y, w[4 * k + 2] = u.z, w[4 * k + 3] = u.w;
         }
     }
-    __device__ __forceinline__ void set(const T *p, int64_t e, int i) {
-        const uint32_t b = Io<T>::bits(p, e);
+    __device__ __forceinline__ void put_bits(int i, uint32_t b) {  // into a cleared place
         if constexpr (sizeof(T) == 4) w[i] = b;
         else w[i >> 1] |= b << (16 * (i & 1));
     }
-    // Elements [lo, hi) of it; the others are zero.
+    // Elements [lo, hi) of it; the others are zero.  Loads without a branch
+    // (from the nearest element of the range), so that all are in flight at
+    // once, then the selection.
     __device__ __forceinline__ void load_part(const T *p, int64_t e, int lo, int hi) {
         clear();
+        if (hi <= lo) return;
+        uint32_t b[kV];
 #pragma unroll
-        for (int i = 0; i < kV; ++i)
-            if (i >= lo && i < hi) set(p, e + i, i);
+        for (int i = 0; i < kV; ++i) b[i] = Io<T>::bits(p, e + (i < lo ? lo : i < hi ? i : hi - 1));
+#pragma unroll
+        for (int i = 0; i < kV; ++i) put_bits(i, i >= lo && i < hi ? b[i] : 0u);
     }
 };
 

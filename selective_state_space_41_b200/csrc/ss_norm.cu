@@ -51,22 +51,23 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Sum of a and b over the T threads of a row (T = 32: a warp; else the block).
+// Sums over the T threads of a row: a warp, or T / 32 warps of the block,
+// which meet at a barrier of their own (`group` counts such groups).
 template <int kN>
-__device__ __forceinline__ void row_sum(float (&v)[kN], int T, float (*red)[kN]) {
+__device__ __forceinline__ void row_sum(float (&v)[kN], int T, int group, float (*red)[kN]) {
 #pragma unroll
     for (int k = 0; k < kN; ++k) v[k] = warp_sum(v[k]);
     if (T == 32) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = T >> 5, first = group * n;
     if (lane == 0) {
 #pragma unroll
         for (int k = 0; k < kN; ++k) red[warp][k] = v[k];
     }
-    __syncthreads();
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(T) : "memory");
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
         float s = 0.f;
-        for (int i = 0; i < (T >> 5); ++i) s += red[i][k];
+        for (int i = 0; i < n; ++i) s += red[first + i][k];
         v[k] = s;
     }
 }
@@ -76,70 +77,75 @@ __device__ __forceinline__ void row_sum(float (&v)[kN], int T, float (*red)[kN])
 // Column of element i of a thread's vector k: vectors of 8, or single
 // elements where rows are not whole vectors or a base is not on 16 bytes.
 template <bool kVec>
-__device__ __forceinline__ int64_t column(int k, int i, int t, int T) {
-    return kVec ? ((int64_t)k * T + t) * kV + i : ((int64_t)k * kV + i) * T + t;
+__device__ __forceinline__ int column(int k, int i, int t, int T) {
+    return kVec ? (k * T + t) * kV + i : (k * kV + i) * T + t;
 }
 
 template <typename T, int kNv, bool kVec>
-__device__ __forceinline__ void load_row(Vec8<T> (&r)[kNv], const T *row, int t, int T_, int64_t dim) {
+__device__ __forceinline__ void load_row(Vec8<T> (&r)[kNv], const T *row, int t, int T_, int dim) {
 #pragma unroll
     for (int k = 0; k < kNv; ++k) {
         r[k].clear();
         if constexpr (kVec) {
-            const int64_t c = column<true>(k, 0, t, T_);
+            const int c = column<true>(k, 0, t, T_);
             if (c < dim) r[k].load(row, c);
         } else {
+            // no branch around a load: all of them are in flight at once
+            uint32_t b[kV];
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
-                const int64_t c = column<false>(k, i, t, T_);
-                if (c < dim) r[k].set(row, c, i);
+                const int c = column<false>(k, i, t, T_);
+                b[i] = Io<T>::bits(row, c < dim ? c : dim - 1);
             }
+#pragma unroll
+            for (int i = 0; i < kV; ++i) r[k].put_bits(i, column<false>(k, i, t, T_) < dim ? b[i] : 0u);
         }
     }
 }
 
 template <bool kVec>
-__device__ __forceinline__ void load_cols(float (&w)[kV], const float *p, int k, int t, int T, int64_t dim, float none) {
+__device__ __forceinline__ void load_cols(float (&w)[kV], const float *p, int k, int t, int T, int dim, float none) {
     if (!p) {
 #pragma unroll
         for (int i = 0; i < kV; ++i) w[i] = none;
     } else if constexpr (kVec) {
-        const int64_t c = column<true>(k, 0, t, T);
-        if (c >= dim) return;
-#pragma unroll
-        for (int i = 0; i < kV; ++i) w[i] = __ldg(p + c + i);
+        int c = column<true>(k, 0, t, T);
+        c = c < dim ? c : dim - kV;
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(p + c)), b = __ldg(reinterpret_cast<const float4 *>(p + c) + 1);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
     } else {
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const int64_t c = column<false>(k, i, t, T);
-            w[i] = c < dim ? __ldg(p + c) : 0.f;
+            const int c = column<false>(k, i, t, T);
+            w[i] = __ldg(p + (c < dim ? c : dim - 1));
         }
     }
 }
 
 template <typename T, bool kVec>
-__device__ __forceinline__ void store_cols(T *row, const float (&v)[kV], int k, int t, int T_, int64_t dim) {
+__device__ __forceinline__ void store_cols(T *row, const float (&v)[kV], int k, int t, int T_, int dim) {
     if constexpr (kVec) {
-        const int64_t c = column<true>(k, 0, t, T_);
+        const int c = column<true>(k, 0, t, T_);
         if (c < dim) store_vec(row + c, v);
     } else {
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const int64_t c = column<false>(k, i, t, T_);
+            const int c = column<false>(k, i, t, T_);
             if (c < dim) put(row, c, v[i]);
         }
     }
 }
 
-// T threads a row; with T = 32 each of the block's warps has a row.
+// T threads a row, blockDim / T rows a block.
 template <typename Tin, typename Tout, int kNv, bool kVec>
 __global__ void __launch_bounds__(512) norm_rows_fwd_kernel(const NormParams p, int T) {
-    __shared__ float red[2][32][1];
-    const int t = T == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t row = T == 32 ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
-    if (row >= p.batch) return;
+    __shared__ float red[2][16][1];
+    const int group = threadIdx.x / T, t = threadIdx.x - group * T;
+    const int dim = (int)p.dim;
+    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / T) + group;
+    if (row >= p.batch) return;  // a whole group, and with it its barrier
     Vec8<Tin> x[kNv];
-    load_row<Tin, kNv, kVec>(x, static_cast<const Tin *>(p.x) + row * p.dim, t, T, p.dim);
+    load_row<Tin, kNv, kVec>(x, static_cast<const Tin *>(p.x) + row * p.dim, t, T, dim);
     float mean = 0.f;
     if (!p.rms) {
         float s[1] = {0.f};
@@ -147,7 +153,7 @@ __global__ void __launch_bounds__(512) norm_rows_fwd_kernel(const NormParams p, 
         for (int k = 0; k < kNv; ++k)
 #pragma unroll
             for (int i = 0; i < kV; ++i) s[0] += x[k][i];
-        row_sum<1>(s, T, red[0]);
+        row_sum<1>(s, T, group, red[0]);
         mean = s[0] * p.inv_dim;
     }
     float q[1] = {0.f};
@@ -156,9 +162,9 @@ __global__ void __launch_bounds__(512) norm_rows_fwd_kernel(const NormParams p, 
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
             const float c = x[k][i] - mean;
-            if (column<kVec>(k, i, t, T) < p.dim) q[0] = fmaf(c, c, q[0]);
+            if (column<kVec>(k, i, t, T) < dim) q[0] = fmaf(c, c, q[0]);
         }
-    row_sum<1>(q, T, red[1]);
+    row_sum<1>(q, T, group, red[1]);
     const float rstd = rsqrtf(fmaf(q[0], p.inv_dim, p.eps));
     if (t == 0) {
         if (p.mean && !p.rms) p.mean[row] = mean;
@@ -168,11 +174,11 @@ __global__ void __launch_bounds__(512) norm_rows_fwd_kernel(const NormParams p, 
 #pragma unroll
     for (int k = 0; k < kNv; ++k) {
         float w[kV], b[kV], v[kV];
-        load_cols<kVec>(w, p.weight, k, t, T, p.dim, 1.f);
-        load_cols<kVec>(b, p.bias, k, t, T, p.dim, 0.f);
+        load_cols<kVec>(w, p.weight, k, t, T, dim, 1.f);
+        load_cols<kVec>(b, p.bias, k, t, T, dim, 0.f);
 #pragma unroll
         for (int i = 0; i < kV; ++i) v[i] = fmaf((x[k][i] - mean) * rstd, w[i], b[i]);
-        store_cols<Tout, kVec>(y, v, k, t, T, p.dim);
+        store_cols<Tout, kVec>(y, v, k, t, T, dim);
     }
 }
 
@@ -186,13 +192,13 @@ __global__ void __launch_bounds__(1024) norm_rows_fwd_wide_kernel(const NormPara
     float s[1] = {0.f}, q[1] = {0.f};
     if (!p.rms)
         for (int64_t c = threadIdx.x; c < p.dim; c += blockDim.x) s[0] += load_elem(x, c);
-    row_sum<1>(s, blockDim.x, red[0]);
+    row_sum<1>(s, blockDim.x, 0, red[0]);
     const float mean = s[0] * p.inv_dim;
     for (int64_t c = threadIdx.x; c < p.dim; c += blockDim.x) {
         const float v = load_elem(x, c) - mean;
         q[0] = fmaf(v, v, q[0]);
     }
-    row_sum<1>(q, blockDim.x, red[1]);
+    row_sum<1>(q, blockDim.x, 0, red[1]);
     const float rstd = rsqrtf(fmaf(q[0], p.inv_dim, p.eps));
     if (threadIdx.x == 0) {
         if (p.mean && !p.rms) p.mean[row] = mean;
@@ -205,31 +211,31 @@ __global__ void __launch_bounds__(1024) norm_rows_fwd_wide_kernel(const NormPara
 
 template <typename Tin, typename Tout, int kNv, bool kVec>
 __global__ void __launch_bounds__(512) norm_rows_bwd_kernel(const NormParams p, int T) {
-    extern __shared__ float acc[];  // T = 32: the warps' sums, joined at the end
-    __shared__ float red[2][32][2];
-    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
-    const int t = T == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t step = T == 32 ? (int64_t)gridDim.x * warps : gridDim.x;
+    extern __shared__ float acc[];  // the groups' sums, joined at the end
+    __shared__ float red[2][16][2];
+    const int groups = blockDim.x / T, group = threadIdx.x / T, t = threadIdx.x - group * T;
+    const int dim = (int)p.dim;
+    const int64_t step = (int64_t)gridDim.x * groups;
     float dw[kNv][kV], db[kNv][kV];
 #pragma unroll
     for (int k = 0; k < kNv; ++k)
 #pragma unroll
         for (int i = 0; i < kV; ++i) dw[k][i] = db[k][i] = 0.f;
     int buf = 0;
-    for (int64_t row = T == 32 ? (int64_t)blockIdx.x * warps + warp : blockIdx.x; row < p.batch; row += step, buf ^= 1) {
+    for (int64_t row = (int64_t)blockIdx.x * groups + group; row < p.batch; row += step, buf ^= 1) {
         Vec8<Tin> x[kNv];
         Vec8<Tout> dy[kNv];
-        load_row<Tin, kNv, kVec>(x, static_cast<const Tin *>(p.x) + row * p.dim, t, T, p.dim);
-        load_row<Tout, kNv, kVec>(dy, static_cast<const Tout *>(p.dy) + row * p.dim, t, T, p.dim);
+        load_row<Tin, kNv, kVec>(x, static_cast<const Tin *>(p.x) + row * p.dim, t, T, dim);
+        load_row<Tout, kNv, kVec>(dy, static_cast<const Tout *>(p.dy) + row * p.dim, t, T, dim);
         const float mean = p.mean_in ? __ldg(p.mean_in + row) : 0.f, rstd = __ldg(p.rstd_in + row);
         float c[2] = {0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < kNv; ++k) {
             float w[kV];
-            load_cols<kVec>(w, p.weight, k, t, T, p.dim, 1.f);
+            load_cols<kVec>(w, p.weight, k, t, T, dim, 1.f);
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
-                if (column<kVec>(k, i, t, T) < p.dim) {
+                if (column<kVec>(k, i, t, T) < dim) {
                     const float g = dy[k][i], xh = (x[k][i] - mean) * rstd, v = g * w[i];
                     c[0] += v;
                     c[1] = fmaf(v, xh, c[1]);
@@ -238,46 +244,47 @@ __global__ void __launch_bounds__(512) norm_rows_bwd_kernel(const NormParams p, 
                 }
             }
         }
-        row_sum<2>(c, T, red[buf]);
+        row_sum<2>(c, T, group, red[buf]);
+#pragma unroll
+        for (int k = 0; k < kNv; ++k) x[k].again(), dy[k].again();
         const float c1 = p.mean_in ? c[0] * p.inv_dim : 0.f, c2 = c[1] * p.inv_dim;
         Tin *dx = static_cast<Tin *>(p.dx) + row * p.dim;
 #pragma unroll
         for (int k = 0; k < kNv; ++k) {
             float w[kV], v[kV];
-            load_cols<kVec>(w, p.weight, k, t, T, p.dim, 1.f);
+            load_cols<kVec>(w, p.weight, k, t, T, dim, 1.f);
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
                 const float xh = (x[k][i] - mean) * rstd;
                 v[i] = (fmaf(dy[k][i], w[i], -c1) - xh * c2) * rstd;
             }
-            store_cols<Tin, kVec>(dx, v, k, t, T, p.dim);
+            store_cols<Tin, kVec>(dx, v, k, t, T, dim);
         }
     }
     if (!p.sums) return;
     float *out = p.part + (int64_t)blockIdx.x * 2 * p.dim;
-    if (T == 32) {
-        // the block's warps hold the same columns
-        for (int w = 0; w < warps; ++w) {
-            if (warp == w) {
+    if (groups > 1) {  // the same columns, one group after the other
+        for (int g = 0; g < groups; ++g) {
+            if (group == g) {
 #pragma unroll
                 for (int k = 0; k < kNv; ++k)
 #pragma unroll
                     for (int i = 0; i < kV; ++i) {
-                        const int64_t c = column<kVec>(k, i, t, 32);
-                        if (c < p.dim) {
-                            acc[c] = w ? acc[c] + dw[k][i] : dw[k][i];
-                            acc[p.dim + c] = w ? acc[p.dim + c] + db[k][i] : db[k][i];
+                        const int c = column<kVec>(k, i, t, T);
+                        if (c < dim) {
+                            acc[c] = g ? acc[c] + dw[k][i] : dw[k][i];
+                            acc[dim + c] = g ? acc[dim + c] + db[k][i] : db[k][i];
                         }
                     }
             }
             __syncthreads();
         }
-        for (int64_t c = threadIdx.x; c < 2 * p.dim; c += blockDim.x) out[c] = acc[c];
+        for (int c = threadIdx.x; c < 2 * dim; c += blockDim.x) out[c] = acc[c];
     } else {
 #pragma unroll
         for (int k = 0; k < kNv; ++k) {
-            store_cols<float, kVec>(out, dw[k], k, t, T, p.dim);
-            store_cols<float, kVec>(out + p.dim, db[k], k, t, T, p.dim);
+            store_cols<float, kVec>(out, dw[k], k, t, T, dim);
+            store_cols<float, kVec>(out + dim, db[k], k, t, T, dim);
         }
     }
 }
@@ -306,7 +313,7 @@ __global__ void __launch_bounds__(1024) norm_rows_bwd_wide_kernel(const NormPara
                 out[p.dim + d] = first ? g : out[p.dim + d] + g;
             }
         }
-        row_sum<2>(c, blockDim.x, red[buf]);
+        row_sum<2>(c, blockDim.x, 0, red[buf]);
         const float c1 = p.mean_in ? c[0] * p.inv_dim : 0.f, c2 = c[1] * p.inv_dim;
         for (int64_t d = threadIdx.x; d < p.dim; d += blockDim.x) {
             const float w = p.weight ? __ldg(p.weight + d) : 1.f, xh = (load_elem(x, d) - mean) * rstd;
@@ -317,118 +324,236 @@ __global__ void __launch_bounds__(1024) norm_rows_bwd_wide_kernel(const NormPara
 
 // ------------------------------------------------------------------ steps
 
-constexpr int kNch = 32;  // channels a lane holds
+constexpr int kWarpCh = 32;  // channels of a warp
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float peer_load(const float *p, int rank) {
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// v into the same place of block `rank`'s shared memory.
+__device__ __forceinline__ void peer_store(float2 *p, int rank, float2 v) {
     uint32_t peer;
-    float v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer) : "memory");
-    return v;
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(peer), "f"(v.x), "f"(v.y) : "memory");
 }
 
-// A step's place: element of channel 0, and whether there is such a step.
-struct Step {
+// V consecutive steps of a channel as they lie in memory: one or two 16-byte
+// words, or a single element.
+template <typename T, int V>
+struct Run {
+    static constexpr int kWords = V * sizeof(T) >= 4 ? V * sizeof(T) / 4 : 1;
+    uint32_t w[kWords];
+    __device__ __forceinline__ float operator[](int i) const { return Io<T>::widen(w, i); }
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (V == 1) {
+            w[0] = Io<T>::bits(p, 0);
+        } else {
+            const uint4 *q = reinterpret_cast<const uint4 *>(p);
+#pragma unroll
+            for (int k = 0; k < kWords / 4; ++k) {
+                const uint4 u = __ldg(q + k);
+                w[4 * k] = u.x, w[4 * k + 1] = u.y, w[4 * k + 2] = u.z, w[4 * k + 3] = u.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) w[k] = 0u;
+    }
+    __device__ __forceinline__ void again() {  // as Vec8::again
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) asm volatile("" : "+r"(w[k]));
+    }
+};
+
+template <int V>
+__device__ __forceinline__ void store_run_of(float *p, const float (&v)[V]) {
+    if constexpr (V == 1) {
+        *p = v[0];
+    } else {
+#pragma unroll
+        for (int k = 0; k < V / 4; ++k)
+            reinterpret_cast<float4 *>(p)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    }
+}
+template <int V>
+__device__ __forceinline__ void store_run_of(__nv_bfloat16 *p, const float (&v)[V]) {
+    if constexpr (V == 1) *p = __float2bfloat16_rn(v[0]);
+    else store_vec(p, v);
+}
+
+// How a warp covers its 32 channels: kLs lanes along the steps, V steps each
+// (16 bytes of the input), and kLc lanes by kN channels.  V = 1 where rows
+// are not whole vectors: then every lane has a step and all 32 channels.
+template <int V>
+struct Tile {
+    static constexpr int kLc = V == 1 ? 1 : 4, kLs = 32 / kLc, kN = kWarpCh / kLc, kSteps = kLs * V;
+};
+
+// Where a lane's steps lie: element of channel 0, index among all steps (the
+// last ones again for a lane behind the end).
+struct Place {
     int64_t at, index;
     bool in;
 };
-__device__ __forceinline__ Step step_of(const NormParams &p, int64_t tile, int lane) {
-    const int64_t s = tile * 32 + lane, n = p.batch * p.L;
-    Step r;
+template <int V>
+__device__ __forceinline__ Place place_of(const NormParams &p, int64_t tile, int sl) {
+    const int64_t s = tile * Tile<V>::kSteps + sl * V, n = p.batch * p.L;
+    Place r;
     r.in = s < n;
-    r.index = r.in ? s : n - 1;
-    const int64_t b = r.index / p.L;
+    r.index = r.in ? s : n - V;
+    const int64_t b = n <= INT_MAX ? (int64_t)((uint32_t)r.index / (uint32_t)p.L) : r.index / p.L;
     r.at = b * p.dim * p.L + (r.index - b * p.L);
     return r;
 }
 
-// Forward over steps: nblk blocks of a cluster share the channels.
-template <typename Tin, typename Tout>
-__global__ void __launch_bounds__(512) norm_steps_fwd_kernel(const NormParams p, int nblk) {
-    __shared__ float sm[2][16][32];  // per warp: mean and squares about it
-    __shared__ float all[2][32];     // the block's
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int rank = (int)(blockIdx.x % nblk);
-    const int64_t c0 = ((int64_t)rank * warps + warp) * kNch;
-    const Step st = step_of(p, blockIdx.x / nblk, lane);
-    const Tin *x = static_cast<const Tin *>(p.x) + st.at;
-    const int have = c0 >= p.dim ? 0 : p.dim - c0 < kNch ? (int)(p.dim - c0) : kNch;
-    float v[kNch];
-#pragma unroll
-    for (int i = 0; i < kNch; ++i) v[i] = i < have ? load_elem(x, (c0 + i) * p.L) : 0.f;
+__device__ __forceinline__ float clamp_count(int64_t n, int64_t most) { return n <= 0 ? 0.f : (float)(n < most ? n : most); }
 
-    // Mean and squares about it, joined from parts (n, m, S):
-    // m = sum n_i m_i / n,  S = sum S_i + sum n_i (m_i - m)^2.
-    const auto count = [&](int64_t first, int64_t width) {  // channels of a part
-        const int64_t k = p.dim - first;
-        return k <= 0 ? 0.f : (float)(k < width ? k : width);
-    };
-    float m = 0.f, S = 0.f;
-    if (!p.rms && have) {
-#pragma unroll
-        for (int i = 0; i < kNch; ++i) m += v[i];
-        m /= (float)have;
-    }
-#pragma unroll
-    for (int i = 0; i < kNch; ++i) {
-        const float c = v[i] - m;
-        if (i < have) S = fmaf(c, c, S);
-    }
-    sm[0][warp][lane] = m, sm[1][warp][lane] = S;
-    __syncthreads();
-    const int64_t b0 = (int64_t)rank * warps * kNch;
-    if (warp == 0) {
-        float n = 0.f, mb = 0.f, Sb = 0.f;
-        for (int k = 0; k < warps; ++k) {
-            const float nk = count(b0 + k * kNch, kNch);
-            mb = fmaf(nk, sm[0][k][lane], mb);
-            n += nk;
-        }
-        mb = n > 0.f ? mb / n : 0.f;
-        for (int k = 0; k < warps; ++k) {
-            const float d = sm[0][k][lane] - mb;
-            Sb += fmaf(count(b0 + k * kNch, kNch) * d, d, sm[1][k][lane]);
-        }
-        all[0][lane] = mb, all[1][lane] = Sb;
-    }
-    if (nblk > 1) cluster_sync();
-    else __syncthreads();
-    float mean = 0.f, sq = 0.f;
-    if (nblk > 1) {
-        const int64_t wide = (int64_t)warps * kNch;
-        for (int k = 0; k < nblk; ++k) mean = fmaf(count(k * wide, wide), peer_load(&all[0][lane], k), mean);
-        mean *= p.inv_dim;
-        for (int k = 0; k < nblk; ++k) {
-            const float d = peer_load(&all[0][lane], k) - mean;
-            sq += fmaf(count(k * wide, wide) * d, d, peer_load(&all[1][lane], k));
-        }
-    } else {
-        mean = all[0][lane], sq = all[1][lane];
-    }
-    if (p.rms) mean = 0.f;
-    const float rstd = rsqrtf(fmaf(sq, p.inv_dim, p.eps));
-    if (st.in && rank == 0 && warp == 0) {
-        if (p.mean && !p.rms) p.mean[st.index] = mean;
-        if (p.rstd) p.rstd[st.index] = rstd;
-    }
-    Tout *y = static_cast<Tout *>(p.y) + st.at;
-#pragma unroll
-    for (int i = 0; i < kNch; ++i) {
-        if (i < have) {
-            const float w = p.weight ? __ldg(p.weight + c0 + i) : 1.f, b = p.bias ? __ldg(p.bias + c0 + i) : 0.f;
-            if (st.in) put(y, (c0 + i) * p.L, fmaf((v[i] - mean) * rstd, w, b));
-        }
-    }
-    if (nblk > 1) cluster_sync();  // no block leaves while its sums may be read
+// Channels of a thread that there are, of c0, c0 + kLc, ...
+template <int V>
+__device__ __forceinline__ int have_of(const NormParams &p, int64_t c0) {
+    using G = Tile<V>;
+    return c0 >= p.dim ? 0 : (int)min((int64_t)G::kN, (p.dim - c0 + G::kLc - 1) / G::kLc);
 }
 
-// Sums over the 32 lanes of kNch values each: value i to lane i.
-__device__ __forceinline__ float lane_sums(float (&v)[kNch], int lane) {
+// Makes a distance opaque: addresses are computed anew from here, rather than
+// kept in registers since the loads.
+__device__ __forceinline__ void again(int64_t &v) { asm volatile("" : "+l"(v)); }
+
+// (n, m, S) and (nb, mb, Sb), number, mean and squares about the mean, into
+// one: m + (mb - m) nb / (n + nb), S + Sb + (mb - m)^2 n nb / (n + nb).
+__device__ __forceinline__ void join(float f, float h, float &m, float &S, float mb, float Sb) {
+    const float d = mb - m;
+    m = fmaf(d, f, m);
+    S += fmaf(d * d, h, Sb);
+}
+
+// Forward over steps.  The statistics of a step come together in four
+// stages, always as mean and squares about it (no difference of large sums):
+// a thread's channels, the kLc lanes, the block's warps, the cluster's
+// blocks; each block writes its own into every other's shared memory, so one
+// cluster barrier is all they wait for.
+template <typename Tin, typename Tout, int V, int kMaxW>
+__global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 3 : 1) norm_steps_fwd_kernel(const NormParams p, int nblk) {
+    using G = Tile<V>;
+    __shared__ float2 part[kMaxW][G::kSteps], slot[8][G::kSteps], stat[G::kSteps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int rank = (int)(blockIdx.x % nblk), sl = lane % G::kLs, cl = lane / G::kLs;
+    if (nblk > 1) cluster_arrive();  // waited for before the first remote store
+    const int64_t c0 = ((int64_t)rank * warps + warp) * kWarpCh + cl;  // channels c0 + i kLc
+    const Place at = place_of<V>(p, blockIdx.x / nblk, sl);
+    const int have = have_of<V>(p, c0);
+    const int64_t first = at.at + min(c0, p.dim - 1) * p.L;
+    const Tin *x = static_cast<const Tin *>(p.x) + first;
+    int64_t apart = G::kLc * p.L;
+    Run<Tin, V> r[G::kN];
 #pragma unroll
-    for (int o = 16; o >= 1; o /= 2) {
+    for (int i = 0; i < G::kN; ++i) r[i].load(x + min(i, max(have - 1, 0)) * apart);
+
+    float m[V], S[V];
+    const float n0 = (float)have, inv0 = have ? 1.f / n0 : 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) m[j] = S[j] = 0.f;
+    if (!p.rms) {
+#pragma unroll
+        for (int i = 0; i < G::kN; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) m[j] += i < have ? r[i][j] : 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) m[j] *= inv0;
+    }
+#pragma unroll
+    for (int i = 0; i < G::kN; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float c = i < have ? r[i][j] - m[j] : 0.f;
+            S[j] = fmaf(c, c, S[j]);
+        }
+    float n = n0;
+#pragma unroll
+    for (int o = G::kLs; o < 32; o *= 2) {
+        const float nb = __shfl_xor_sync(0xffffffffu, n, o), both = n + nb;
+        const float f = both > 0.f ? nb / both : 0.f, h = n * f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float mb = __shfl_xor_sync(0xffffffffu, m[j], o), Sb = __shfl_xor_sync(0xffffffffu, S[j], o);
+            join(f, h, m[j], S[j], mb, Sb);
+        }
+        n = both;
+    }
+    if (cl == 0) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) part[warp][sl * V + j] = make_float2(m[j], S[j]);
+    }
+    __syncthreads();
+    const int t = threadIdx.x;
+    const int64_t wide = (int64_t)warps * kWarpCh;
+    float2 all = make_float2(0.f, 0.f);
+    if (t < G::kSteps) {
+        float nn = 0.f;
+        for (int k = 0; k < warps; ++k) {
+            const float nk = clamp_count(p.dim - (rank * wide + k * kWarpCh), kWarpCh), both = nn + nk;
+            const float f = both > 0.f ? nk / both : 0.f;
+            join(f, nn * f, all.x, all.y, part[k][t].x, part[k][t].y);
+            nn = both;
+        }
+    }
+    if (nblk > 1) {
+        cluster_wait();  // every block has begun
+        if (t < G::kSteps)
+            for (int k = 0; k < nblk; ++k) peer_store(&slot[rank][t], k, all);
+        cluster_arrive();
+        cluster_wait();
+        if (t < G::kSteps) {
+            float nn = 0.f;
+            all = make_float2(0.f, 0.f);
+            for (int k = 0; k < nblk; ++k) {
+                const float nk = clamp_count(p.dim - k * wide, wide), both = nn + nk;
+                const float f = both > 0.f ? nk / both : 0.f;
+                join(f, nn * f, all.x, all.y, slot[k][t].x, slot[k][t].y);
+                nn = both;
+            }
+        }
+    }
+    if (t < G::kSteps) {
+        const float rstd = rsqrtf(fmaf(all.y, p.inv_dim, p.eps));
+        stat[t] = make_float2(all.x, rstd);
+        const int64_t s = (blockIdx.x / nblk) * (int64_t)G::kSteps + t;
+        if (rank == 0 && s < p.batch * p.L) {
+            if (p.mean && !p.rms) p.mean[s] = all.x;
+            if (p.rstd) p.rstd[s] = rstd;
+        }
+    }
+    __syncthreads();
+    if (!at.in) return;
+#pragma unroll
+    for (int i = 0; i < G::kN; ++i) r[i].again();
+    float rstd[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const float2 q = stat[sl * V + j];
+        m[j] = q.x, rstd[j] = q.y;
+    }
+    Tout *y = static_cast<Tout *>(p.y) + first;
+    again(apart);
+#pragma unroll
+    for (int i = 0; i < G::kN; ++i) {
+        if (i < have) {
+            const int64_t c = c0 + i * G::kLc;
+            const float w = p.weight ? __ldg(p.weight + c) : 1.f, b = p.bias ? __ldg(p.bias + c) : 0.f;
+            float v[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = fmaf((r[i][j] - m[j]) * rstd[j], w, b);
+            store_run_of<V>(y + i * apart, v);
+        }
+    }
+}
+
+// Sums over kN neighbouring lanes of kN values each, value i to lane i of them:
+// each round halves the values a lane still holds.
+template <int kN>
+__device__ __forceinline__ float lane_sums(float (&v)[kN], int lane) {
+#pragma unroll
+    for (int o = kN / 2; o >= 1; o /= 2) {
         const bool up = lane & o;
 #pragma unroll
         for (int k = 0; k < o; ++k) {
@@ -439,81 +564,138 @@ __device__ __forceinline__ float lane_sums(float (&v)[kNch], int lane) {
     return v[0];
 }
 
-template <typename Tin, typename Tout>
-__global__ void __launch_bounds__(512) norm_steps_bwd_kernel(const NormParams p, int nblk) {
-    __shared__ float sm[2][16][32];
-    __shared__ float all[2][2][32];
+// Backward over steps: clusters stay and walk over the tiles.
+template <typename Tin, typename Tout, int V, int kMaxW>
+__global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 2 : 1) norm_steps_bwd_kernel(const NormParams p, int nblk) {
+    using G = Tile<V>;
+    static_assert(G::kN == G::kLs, "one channel's sum for each step lane");
+    __shared__ float2 part[kMaxW][G::kSteps], slot[2][8][G::kSteps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int rank = (int)(blockIdx.x % nblk);
+    const int rank = (int)(blockIdx.x % nblk), sl = lane % G::kLs, cl = lane / G::kLs;
     const int64_t group = blockIdx.x / nblk, groups = gridDim.x / nblk;
-    const int64_t c0 = ((int64_t)rank * warps + warp) * kNch;
-    const int have = c0 >= p.dim ? 0 : p.dim - c0 < kNch ? (int)(p.dim - c0) : kNch;
-    const int64_t tiles = (p.batch * p.L + 31) / 32;
-    float dw = 0.f, db = 0.f;  // of channel c0 + lane
+    const int64_t c0 = ((int64_t)rank * warps + warp) * kWarpCh + cl;
+    const int have = have_of<V>(p, c0);
+    const int64_t tiles = (p.batch * p.L + G::kSteps - 1) / G::kSteps;
+    if (nblk > 1) cluster_arrive();
+    bool begun = nblk == 1;
+    float dw = 0.f, db = 0.f;  // of channel c0 + sl kLc
     int buf = 0;
     for (int64_t tile = group; tile < tiles; tile += groups, buf ^= 1) {
-        const Step st = step_of(p, tile, lane);
-        const Tin *x = static_cast<const Tin *>(p.x) + st.at;
-        const Tout *dy = static_cast<const Tout *>(p.dy) + st.at;
-        float xh[kNch], g[kNch];
+        const Place at = place_of<V>(p, tile, sl);
+        const int64_t first = at.at + min(c0, p.dim - 1) * p.L;
+        const Tin *x = static_cast<const Tin *>(p.x) + first;
+        const Tout *dy = static_cast<const Tout *>(p.dy) + first;
+        int64_t apart = G::kLc * p.L, wc = c0;  // (made opaque: not kept in registers from tile to tile)
+        again(apart), again(wc);
+        Run<Tin, V> rx[G::kN];
+        Run<Tout, V> rg[G::kN];
 #pragma unroll
-        for (int i = 0; i < kNch; ++i) {
-            xh[i] = i < have ? load_elem(x, (c0 + i) * p.L) : 0.f;
-            g[i] = i < have && st.in ? load_elem(dy, (c0 + i) * p.L) : 0.f;
+        for (int i = 0; i < G::kN; ++i) {
+            const int64_t c = min(i, max(have - 1, 0)) * apart;
+            rx[i].load(x + c);
+            rg[i].load(dy + c);
         }
-        const float mean = p.mean_in ? __ldg(p.mean_in + st.index) : 0.f, rstd = __ldg(p.rstd_in + st.index);
-        float s1 = 0.f, s2 = 0.f;
+        float m[V], rstd[V], s1[V], s2[V];
 #pragma unroll
-        for (int i = 0; i < kNch; ++i) {
-            if (i < have) {
-                xh[i] = (xh[i] - mean) * rstd;
-                const float v = p.weight ? g[i] * __ldg(p.weight + c0 + i) : g[i];
-                s1 += v;
-                s2 = fmaf(v, xh[i], s2);
-            }
+        for (int j = 0; j < V; ++j) {
+            m[j] = p.mean_in ? __ldg(p.mean_in + at.index + j) : 0.f;
+            rstd[j] = __ldg(p.rstd_in + at.index + j);
+            s1[j] = s2[j] = 0.f;
         }
-        sm[0][warp][lane] = s1, sm[1][warp][lane] = s2;
-        __syncthreads();
-        if (warp < 2) {
-            float s = 0.f;
-            for (int k = 0; k < warps; ++k) s += sm[warp][k][lane];
-            all[buf][warp][lane] = s;
-        }
-        // one barrier a tile: the two buffers keep a slow block's reads apart from the next tile's sums
-        if (nblk > 1) cluster_sync();
-        else __syncthreads();
-        float c1 = 0.f, c2 = 0.f;
-        if (nblk > 1) {
-            for (int k = 0; k < nblk; ++k) {
-                c1 += peer_load(&all[buf][0][lane], k);
-                c2 += peer_load(&all[buf][1][lane], k);
-            }
-        } else {
-            c1 = all[buf][0][lane], c2 = all[buf][1][lane];
-        }
-        c1 = p.mean_in ? c1 * p.inv_dim : 0.f;
-        c2 *= p.inv_dim;
-        Tin *dx = static_cast<Tin *>(p.dx) + st.at;
 #pragma unroll
-        for (int i = 0; i < kNch; ++i) {
-            if (i < have) {
-                const float w = p.weight ? __ldg(p.weight + c0 + i) : 1.f;
-                if (st.in) put(dx, (c0 + i) * p.L, (fmaf(g[i], w, -c1) - xh[i] * c2) * rstd);
+        for (int i = 0; i < G::kN; ++i) {
+            if (i >= have) rx[i].clear();
+            if (i >= have || !at.in) rg[i].clear();
+        }
+        float term[G::kN];
+#pragma unroll
+        for (int i = 0; i < G::kN; ++i) {
+            const float w = p.weight ? __ldg(p.weight + min(wc + i * G::kLc, p.dim - 1)) : 1.f;
+            term[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float g = rg[i][j], xh = (rx[i][j] - m[j]) * rstd[j], t = g * xh;
+                s1[j] = fmaf(g, w, s1[j]);
+                s2[j] = fmaf(t, w, s2[j]);
+                term[i] += t;
             }
         }
         if (p.sums) {
+            dw += lane_sums<G::kN>(term, lane);
 #pragma unroll
-            for (int i = 0; i < kNch; ++i) xh[i] = st.in ? xh[i] * g[i] : 0.f;
-            dw += lane_sums(xh, lane);
-            db += lane_sums(g, lane);
+            for (int i = 0; i < G::kN; ++i) {
+                term[i] = rg[i][0];
+#pragma unroll
+                for (int j = 1; j < V; ++j) term[i] += rg[i][j];
+            }
+            db += lane_sums<G::kN>(term, lane);
+        }
+#pragma unroll
+        for (int o = G::kLs; o < 32; o *= 2) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                s1[j] += __shfl_xor_sync(0xffffffffu, s1[j], o);
+                s2[j] += __shfl_xor_sync(0xffffffffu, s2[j], o);
+            }
+        }
+        if (cl == 0) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) part[warp][sl * V + j] = make_float2(s1[j], s2[j]);
+        }
+        __syncthreads();
+        const int t = threadIdx.x;
+        float2 all = make_float2(0.f, 0.f);
+        if (t < G::kSteps)
+            for (int k = 0; k < warps; ++k) all.x += part[k][t].x, all.y += part[k][t].y;
+        if (nblk > 1) {
+            if (!begun) cluster_wait();  // every block has begun
+            begun = true;
+            if (t < G::kSteps)
+                for (int k = 0; k < nblk; ++k) peer_store(&slot[buf][rank][t], k, all);
+            // One barrier a tile: a block that is ahead writes the other
+            // half of `slot`, and cannot come back to this one before all
+            // have read it and arrived at the next tile's barrier.
+            cluster_arrive();
+            cluster_wait();
+        } else {
+            if (t < G::kSteps) slot[buf][0][t] = all;
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < G::kN; ++i) rx[i].again(), rg[i].again();
+        if (at.in) {
+            // dx = rstd v - rstd c1 - (x - m) rstd^2 c2, with the step's
+            // factors made once
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float2 c = make_float2(0.f, 0.f);
+                for (int k = 0; k < nblk; ++k) {
+                    const float2 q = slot[buf][k][sl * V + j];
+                    c.x += q.x, c.y += q.y;
+                }
+                s1[j] = p.mean_in ? c.x * p.inv_dim * rstd[j] : 0.f;
+                s2[j] = c.y * p.inv_dim * rstd[j] * rstd[j];
+            }
+            Tin *dx = static_cast<Tin *>(p.dx) + first;
+            again(apart), again(wc);
+#pragma unroll
+            for (int i = 0; i < G::kN; ++i) {
+                if (i < have) {
+                    const float w = p.weight ? __ldg(p.weight + wc + i * G::kLc) : 1.f;
+                    float v[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        v[j] = fmaf(rg[i][j] * w, rstd[j], -s1[j]) - (rx[i][j] - m[j]) * s2[j];
+                    store_run_of<V>(dx + i * apart, v);
+                }
+            }
         }
     }
-    if (p.sums && lane < have) {
+    if (p.sums && sl < have) {
         float *out = p.part + group * 2 * p.dim;
-        out[c0 + lane] = dw;
-        out[p.dim + c0 + lane] = db;
+        out[c0 + sl * G::kLc] = dw;
+        out[p.dim + c0 + sl * G::kLc] = db;
     }
-    if (nblk > 1) cluster_sync();
 }
 
 // More channels than a cluster's registers hold: passes over the tile, the
@@ -522,7 +704,7 @@ template <typename Tin, typename Tout>
 __global__ void __launch_bounds__(512) norm_steps_fwd_wide_kernel(const NormParams p) {
     __shared__ float sm[2][16][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const Step st = step_of(p, blockIdx.x, lane);
+    const Place st = place_of<1>(p, blockIdx.x, lane);
     const Tin *x = static_cast<const Tin *>(p.x) + st.at;
     float mean = 0.f, s = 0.f;
     if (!p.rms) {
@@ -562,7 +744,7 @@ __global__ void __launch_bounds__(512) norm_steps_bwd_wide_kernel(const NormPara
     int buf = 0;
     bool first = true;
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1, first = false) {
-        const Step st = step_of(p, tile, lane);
+        const Place st = place_of<1>(p, tile, lane);
         const Tin *x = static_cast<const Tin *>(p.x) + st.at;
         const Tout *dy = static_cast<const Tout *>(p.dy) + st.at;
         Tin *dx = static_cast<Tin *>(p.dx) + st.at;
@@ -595,23 +777,24 @@ __global__ void __launch_bounds__(512) norm_steps_bwd_wide_kernel(const NormPara
     }
 }
 
-// dw and db from the rows of partial sums, in order: 32 columns by 8 runs of
-// rows per block, the runs joined in shared memory.
-__global__ void __launch_bounds__(256) norm_sums_kernel(const float *part, int64_t parts, int64_t dim, float *dweight,
-                                                        float *dbias) {
-    __shared__ float sm[8][33];
+// dw and db from the rows of partial sums: 32 columns by 32 runs of rows per
+// block, each run and then the runs added in order.
+__global__ void __launch_bounds__(1024) norm_sums_kernel(const float *part, int64_t parts, int64_t dim, float *dweight,
+                                                         float *dbias) {
+    __shared__ float sm[32][33];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + tx;
     float s = 0.f;
     if (c < 2 * dim) {
-#pragma unroll 4
-        for (int64_t k = ty; k < parts; k += 8) s += part[k * 2 * dim + c];
+#pragma unroll 8
+        for (int64_t k = ty; k < parts; k += 32) s += part[k * 2 * dim + c];
     }
     sm[ty][tx] = s;
     __syncthreads();
     if (ty == 0 && c < 2 * dim) {
         float v = 0.f;
-        for (int k = 0; k < 8; ++k) v += sm[k][tx];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v += sm[k][tx];
         if (c < dim) {
             if (dweight) dweight[c] = v;
         } else if (dbias) {
@@ -625,41 +808,55 @@ __global__ void __launch_bounds__(256) norm_sums_kernel(const float *part, int64
 // The launch of a shape: kernel family, threads and blocks.
 struct NormPlan {
     bool rows, wide;
-    int T, nv;         // rows: threads per row, vectors per thread
-    int warps, nblk;   // steps: warps per block, blocks per cluster
+    int T, nv, per;    // rows: threads per row, vectors per thread, rows per block
+    int V, steps;      // steps: of a lane's run, of a tile
+    int warps, max_warps, nblk;  // warps per block, blocks per cluster
     int64_t parts;     // backward: rows of partial sums (blocks or clusters)
 };
 
-constexpr int kRowWarps = 4;  // rows per block where a warp takes a row
+constexpr int kRowThreads = 256;  // of a block, unless one row takes more
 
-NormPlan norm_plan(const ss_desc *desc) {
+NormPlan norm_plan(const ss_desc *desc, bool vec) {
     NormPlan pl{};
     const int64_t sms = layer_sm_count();
     pl.rows = desc->seqlen == 1;
     if (pl.rows) {
-        // The fewest threads whose vectors (four each at most) hold the row.
-        const int64_t vecs = (desc->dim + kV - 1) / kV;
+        // The fewest threads that hold a row with four vectors each at most
+        // (two where elements are loaded one by one and cost more registers).
+        const int64_t vecs = (desc->dim + kV - 1) / kV, most = vec ? 4 : 2;
         pl.T = 32;
-        while (pl.T < 512 && vecs > (int64_t)pl.T * 4) pl.T *= 2;
+        while (pl.T < 512 && vecs > (int64_t)pl.T * most) pl.T *= 2;
         pl.nv = (int)((vecs + pl.T - 1) / pl.T);
-        pl.wide = pl.nv > 4;
-        const int per = !pl.wide && pl.T == 32 ? kRowWarps : 1;
-        const int64_t blocks = (desc->batch + per - 1) / per;
-        const int64_t most = pl.wide ? sms : sms * (pl.T <= 64 ? 8 : pl.T <= 128 ? 6 : pl.T <= 256 ? 3 : 1);
-        pl.parts = blocks < most ? blocks : most;
+        pl.wide = pl.nv > most;
+        pl.per = pl.wide || pl.T > kRowThreads ? 1 : kRowThreads / pl.T;
+        const int64_t blocks = (desc->batch + pl.per - 1) / pl.per;
+        const int64_t resident = pl.wide || pl.T > kRowThreads ? sms : 2 * sms;
+        pl.parts = blocks < resident ? blocks : resident;
     } else {
-        // The channels over the warps of up to 8 blocks, 8 warps each or 16.
-        const int64_t need = (desc->dim + kNch - 1) / kNch;
-        pl.warps = need <= 8 ? (int)need : need <= 64 ? 8 : 16;
-        if (pl.warps < 2) pl.warps = 2;
-        const int64_t nblk = (need + pl.warps - 1) / pl.warps;
+        pl.V = !vec ? 1 : desc->in_dtype == SS_BF16 ? 8 : 4;
+        pl.steps = pl.V == 8 ? 64 : 32;
+        // The channels over up to 8 blocks of 8 warps, or of 16.
+        const int64_t need = (desc->dim + kWarpCh - 1) / kWarpCh;
+        pl.max_warps = need <= 64 ? 8 : 16;
+        const int64_t nblk = (need + pl.max_warps - 1) / pl.max_warps;
         pl.wide = nblk > 8;
         pl.nblk = pl.wide ? 1 : (int)nblk;
-        const int64_t tiles = (desc->batch * desc->seqlen + 31) / 32;
-        const int64_t most = pl.wide ? sms : (sms * 2 * 8 / pl.warps + pl.nblk - 1) / pl.nblk;
-        pl.parts = tiles < most ? tiles : most;
+        pl.warps = pl.wide ? 16 : (int)((need + nblk - 1) / nblk);
+        if (pl.warps < 2) pl.warps = 2;  // a thread for each step of the tile
+        if (pl.wide) pl.steps = 32, pl.V = 1;
+        const int64_t tiles = (desc->batch * desc->seqlen + pl.steps - 1) / pl.steps;
+        const int64_t resident = (sms * (pl.max_warps == 8 ? 2 : 1) + pl.nblk - 1) / pl.nblk;
+        const int64_t rounds = (tiles + resident - 1) / resident;
+        pl.parts = rounds > 0 ? (tiles + rounds - 1) / rounds : 0;
     }
     return pl;
+}
+
+// Whole vectors: rows of dim elements, or steps of each channel.
+bool norm_vec(const ss_desc *desc, std::initializer_list<const void *> ps) {
+    const int64_t inner = desc->seqlen == 1 ? desc->dim : desc->seqlen;
+    const int64_t unit = desc->seqlen == 1 || desc->in_dtype == SS_BF16 ? 8 : 4;
+    return inner % unit == 0 && vec_ok(ps);
 }
 
 template <typename K>
@@ -679,40 +876,48 @@ cudaError_t launch_cluster(K kernel, int64_t grid, int threads, int nblk, cudaSt
 
 template <typename Tin, typename Tout, int kNv, bool kVec>
 cudaError_t launch_rows(bool back, const NormPlan &pl, cudaStream_t s, const NormParams &p) {
-    const int threads = pl.T == 32 ? 32 * kRowWarps : pl.T;
+    const int threads = pl.T * pl.per;
     if (back) {
-        const size_t smem = pl.T == 32 ? (size_t)p.dim * 2 * sizeof(float) : 0;
+        const size_t smem = pl.per > 1 ? (size_t)p.dim * 2 * sizeof(float) : 0;  // at most 32 KB (T = 128)
         norm_rows_bwd_kernel<Tin, Tout, kNv, kVec><<<(unsigned)pl.parts, threads, smem, s>>>(p, pl.T);
     } else {
-        const int64_t grid = pl.T == 32 ? (p.batch + kRowWarps - 1) / kRowWarps : p.batch;
+        const int64_t grid = (p.batch + pl.per - 1) / pl.per;
         norm_rows_fwd_kernel<Tin, Tout, kNv, kVec><<<(unsigned)grid, threads, 0, s>>>(p, pl.T);
     }
     return cudaGetLastError();
 }
 
+template <typename Tin, typename Tout, int V, int kMaxW>
+cudaError_t launch_steps(bool back, const NormPlan &pl, cudaStream_t s, const NormParams &p) {
+    if (back)
+        return launch_cluster(norm_steps_bwd_kernel<Tin, Tout, V, kMaxW>, pl.parts * pl.nblk, 32 * pl.warps, pl.nblk, s, p);
+    const int64_t tiles = (p.batch * p.L + pl.steps - 1) / pl.steps;
+    return launch_cluster(norm_steps_fwd_kernel<Tin, Tout, V, kMaxW>, tiles * pl.nblk, 32 * pl.warps, pl.nblk, s, p);
+}
+
 template <typename Tin, typename Tout>
 cudaError_t dispatch_norm(bool back, bool vec, const NormPlan &pl, cudaStream_t s, const NormParams &p) {
-    if (pl.rows && pl.wide) {
-        if (back) norm_rows_bwd_wide_kernel<Tin, Tout><<<(unsigned)pl.parts, 1024, 0, s>>>(p);
-        else norm_rows_fwd_wide_kernel<Tin, Tout><<<(unsigned)p.batch, 1024, 0, s>>>(p);
+    if (pl.wide) {
+        if (pl.rows && back) norm_rows_bwd_wide_kernel<Tin, Tout><<<(unsigned)pl.parts, 1024, 0, s>>>(p);
+        else if (pl.rows) norm_rows_fwd_wide_kernel<Tin, Tout><<<(unsigned)p.batch, 1024, 0, s>>>(p);
+        else if (back) norm_steps_bwd_wide_kernel<Tin, Tout><<<(unsigned)pl.parts, 512, 0, s>>>(p);
+        else norm_steps_fwd_wide_kernel<Tin, Tout><<<(unsigned)((p.batch * p.L + 31) / 32), 512, 0, s>>>(p);
         return cudaGetLastError();
     }
     if (pl.rows) {
+        if (!vec)
+            return pl.nv == 1 ? launch_rows<Tin, Tout, 1, false>(back, pl, s, p) : launch_rows<Tin, Tout, 2, false>(back, pl, s, p);
         switch (pl.nv) {
-            case 1: return vec ? launch_rows<Tin, Tout, 1, true>(back, pl, s, p) : launch_rows<Tin, Tout, 1, false>(back, pl, s, p);
-            case 2: return vec ? launch_rows<Tin, Tout, 2, true>(back, pl, s, p) : launch_rows<Tin, Tout, 2, false>(back, pl, s, p);
-            case 3: return vec ? launch_rows<Tin, Tout, 3, true>(back, pl, s, p) : launch_rows<Tin, Tout, 3, false>(back, pl, s, p);
-            default: return vec ? launch_rows<Tin, Tout, 4, true>(back, pl, s, p) : launch_rows<Tin, Tout, 4, false>(back, pl, s, p);
+            case 1: return launch_rows<Tin, Tout, 1, true>(back, pl, s, p);
+            case 2: return launch_rows<Tin, Tout, 2, true>(back, pl, s, p);
+            case 3: return launch_rows<Tin, Tout, 3, true>(back, pl, s, p);
+            default: return launch_rows<Tin, Tout, 4, true>(back, pl, s, p);
         }
     }
-    const int64_t tiles = (p.batch * p.L + 31) / 32;
-    if (pl.wide) {
-        if (back) norm_steps_bwd_wide_kernel<Tin, Tout><<<(unsigned)pl.parts, 512, 0, s>>>(p);
-        else norm_steps_fwd_wide_kernel<Tin, Tout><<<(unsigned)tiles, 512, 0, s>>>(p);
-        return cudaGetLastError();
-    }
-    if (back) return launch_cluster(norm_steps_bwd_kernel<Tin, Tout>, pl.parts * pl.nblk, 32 * pl.warps, pl.nblk, s, p);
-    return launch_cluster(norm_steps_fwd_kernel<Tin, Tout>, tiles * pl.nblk, 32 * pl.warps, pl.nblk, s, p);
+    constexpr int kWhole = sizeof(Tin) == 2 ? 8 : 4;
+    if (pl.max_warps == 8)
+        return pl.V == 1 ? launch_steps<Tin, Tout, 1, 8>(back, pl, s, p) : launch_steps<Tin, Tout, kWhole, 8>(back, pl, s, p);
+    return pl.V == 1 ? launch_steps<Tin, Tout, 1, 16>(back, pl, s, p) : launch_steps<Tin, Tout, kWhole, 16>(back, pl, s, p);
 }
 
 ss_status check_norm(const ss_desc *desc, LayerSizes *sz) {
@@ -752,15 +957,17 @@ ss_status ss_norm_fwd(const ss_desc *desc, const void *x, const float *weight, c
     NormParams p = norm_params(desc);
     p.x = x, p.weight = weight, p.bias = bias, p.y = y, p.mean = mean, p.rstd = rstd;
     p.eps = eps, p.rms = rms != 0;
-    const bool vec = desc->dim % kV == 0 && vec_ok({x, y});
-    return status_of(SS_LAYER_DISPATCH(desc, dispatch_norm)(false, vec, norm_plan(desc),
+    const bool vec = norm_vec(desc, {x, y, weight, bias});
+    return status_of(SS_LAYER_DISPATCH(desc, dispatch_norm)(false, vec, norm_plan(desc, vec),
                                                             reinterpret_cast<cudaStream_t>(stream), p));
 }
 
 size_t ss_norm_bwd_workspace_bytes(const ss_desc *desc) {
     LayerSizes sz;
     if (check_norm(desc, &sz) != SS_OK || sz.elems == 0) return 0;
-    return (size_t)norm_plan(desc).parts * 2 * (size_t)desc->dim * sizeof(float);
+    // the larger of the two shapes: which one runs depends on the pointers too
+    const int64_t a = norm_plan(desc, false).parts, b = norm_plan(desc, true).parts;
+    return (size_t)(a > b ? a : b) * 2 * (size_t)desc->dim * sizeof(float);
 }
 
 ss_status ss_norm_bwd(const ss_desc *desc, const void *x, const float *weight, const float *mean, const float *rstd,
@@ -782,7 +989,6 @@ ss_status ss_norm_bwd(const ss_desc *desc, const void *x, const float *weight, c
     if (!x || !rstd || !dy || !dx) return SS_ERR_NULL_POINTER;
     const size_t ein = layer_size(desc->in_dtype), eout = layer_size(desc->out_dtype);
     if (!layer_aligned(x, ein) || !layer_aligned(dy, eout) || !layer_aligned(dx, ein)) return SS_ERR_MISALIGNED;
-    const NormPlan pl = norm_plan(desc);
     NormParams p = norm_params(desc);
     p.sums = dweight || dbias;
     if (p.sums) {
@@ -791,10 +997,12 @@ ss_status ss_norm_bwd(const ss_desc *desc, const void *x, const float *weight, c
     }
     p.x = x, p.weight = weight, p.mean_in = mean, p.rstd_in = rstd, p.dy = dy, p.dx = dx;
     p.part = static_cast<float *>(workspace);
-    const bool vec = desc->dim % kV == 0 && vec_ok({x, dy, dx});
+    // dw and db are only written by elements, so weight is the one parameter read in vectors
+    const bool vec = norm_vec(desc, {x, dy, dx, weight, workspace});
+    const NormPlan pl = norm_plan(desc, vec);
     cudaError_t e = SS_LAYER_DISPATCH(desc, dispatch_norm)(true, vec, pl, s, p);
     if (e == cudaSuccess && p.sums) {
-        norm_sums_kernel<<<(unsigned)((2 * p.dim + 31) / 32), 256, 0, s>>>(p.part, pl.parts, p.dim, dweight, dbias);
+        norm_sums_kernel<<<(unsigned)((2 * p.dim + 31) / 32), 1024, 0, s>>>(p.part, pl.parts, p.dim, dweight, dbias);
         e = cudaGetLastError();
     }
     return status_of(e);
