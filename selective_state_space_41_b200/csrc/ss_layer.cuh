@@ -25,12 +25,25 @@ namespace selscan {
 
 constexpr int kV = 8;  // elements per vector: 16 bytes of bf16, 32 of fp32
 
+// Two neighbouring elements of words as they lie in memory, as floats.
+template <typename T>
+__device__ __forceinline__ float2 pair_of(const uint32_t *w, int k) {
+    if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+    else return make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+
 // Eight elements as they lie in memory.
 template <typename T>
 struct Vec8 {
     static constexpr int kWords = kV * sizeof(T) / 4;
     uint32_t w[kWords];
     __device__ __forceinline__ float operator[](int i) const { return Io<T>::widen(w, i); }
+    __device__ __forceinline__ float2 pair(int k) const { return pair_of<T>(w, k); }
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int k = 0; k < kWords; ++k) w[k] = 0u;

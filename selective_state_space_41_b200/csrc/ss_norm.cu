@@ -104,21 +104,22 @@ __device__ __forceinline__ void load_row(Vec8<T> (&r)[kNv], const T *row, int t,
 }
 
 template <bool kVec>
-__device__ __forceinline__ void load_cols(float (&w)[kV], const float *p, int k, int t, int T, int dim, float none) {
+__device__ __forceinline__ void load_cols(float2 (&w)[kV / 2], const float *p, int k, int t, int T, int dim, float none) {
     if (!p) {
 #pragma unroll
-        for (int i = 0; i < kV; ++i) w[i] = none;
+        for (int i = 0; i < kV / 2; ++i) w[i] = both(none);
     } else if constexpr (kVec) {
         int c = column<true>(k, 0, t, T);
         c = c < dim ? c : dim - kV;
         const float4 a = __ldg(reinterpret_cast<const float4 *>(p + c)), b = __ldg(reinterpret_cast<const float4 *>(p + c) + 1);
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+        w[0] = make_float2(a.x, a.y), w[1] = make_float2(a.z, a.w);
+        w[2] = make_float2(b.x, b.y), w[3] = make_float2(b.z, b.w);
     } else {
+        float v[kV];
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const int c = column<false>(k, i, t, T);
-            w[i] = __ldg(p + (c < dim ? c : dim - 1));
-        }
+        for (int i = 0; i < kV; ++i) v[i] = __ldg(p + min(column<false>(k, i, t, T), dim - 1));
+#pragma unroll
+        for (int i = 0; i < kV / 2; ++i) w[i] = make_float2(v[2 * i], v[2 * i + 1]);
     }
 }
 
@@ -136,49 +137,77 @@ __device__ __forceinline__ void store_cols(T *row, const float (&v)[kV], int k, 
     }
 }
 
-// T threads a row, blockDim / T rows a block.
+// Which of a thread's elements there are: all of a vector or none, or one by one.
+template <bool kVec>
+__device__ __forceinline__ float2 there(float2 v, int k, int i, int t, int T, int dim) {
+    if constexpr (kVec) {
+        if (column<true>(k, 0, t, T) >= dim) v = both(0.f);
+    } else {
+        if (column<false>(k, 2 * i, t, T) >= dim) v.x = 0.f;
+        if (column<false>(k, 2 * i + 1, t, T) >= dim) v.y = 0.f;
+    }
+    return v;
+}
+
+// T threads a row, blockDim / T rows a block at a time; the next row is on
+// its way while one is worked on.
 template <typename Tin, typename Tout, int kNv, bool kVec>
 __global__ void __launch_bounds__(512) norm_rows_fwd_kernel(const NormParams p, int T) {
-    __shared__ float red[2][16][1];
-    const int group = threadIdx.x / T, t = threadIdx.x - group * T;
-    const int dim = (int)p.dim;
-    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / T) + group;
+    __shared__ float red[2][2][16][1];
+    const int groups = blockDim.x / T, group = threadIdx.x / T, t = threadIdx.x - group * T, dim = (int)p.dim;
+    const int64_t step = (int64_t)gridDim.x * groups;
+    int64_t row = (int64_t)blockIdx.x * groups + group;
     if (row >= p.batch) return;  // a whole group, and with it its barrier
-    Vec8<Tin> x[kNv];
-    load_row<Tin, kNv, kVec>(x, static_cast<const Tin *>(p.x) + row * p.dim, t, T, dim);
-    float mean = 0.f;
-    if (!p.rms) {
-        float s[1] = {0.f};
+    float2 w[kNv][kV / 2], b[kNv][kV / 2];
+#pragma unroll
+    for (int k = 0; k < kNv; ++k) {
+        load_cols<kVec>(w[k], p.weight, k, t, T, dim, 1.f);
+        load_cols<kVec>(b[k], p.bias, k, t, T, dim, 0.f);
+    }
+    Vec8<Tin> x[kNv], next[kNv];
+    load_row<Tin, kNv, kVec>(next, static_cast<const Tin *>(p.x) + row * p.dim, t, T, dim);
+    for (int buf = 0; row < p.batch; row += step, buf ^= 1) {
+#pragma unroll
+        for (int k = 0; k < kNv; ++k) x[k] = next[k];
+        if (row + step < p.batch)
+            load_row<Tin, kNv, kVec>(next, static_cast<const Tin *>(p.x) + (row + step) * p.dim, t, T, dim);
+        float2 nm = both(0.f);
+        if (!p.rms) {
+            float2 s = both(0.f);
+#pragma unroll
+            for (int k = 0; k < kNv; ++k)
+#pragma unroll
+                for (int i = 0; i < kV / 2; ++i) s = add2(s, x[k].pair(i));
+            float v[1] = {s.x + s.y};
+            row_sum<1>(v, T, group, red[buf][0]);
+            nm = both(-v[0] * p.inv_dim);
+        }
+        float2 q = both(0.f);
 #pragma unroll
         for (int k = 0; k < kNv; ++k)
 #pragma unroll
-            for (int i = 0; i < kV; ++i) s[0] += x[k][i];
-        row_sum<1>(s, T, group, red[0]);
-        mean = s[0] * p.inv_dim;
-    }
-    float q[1] = {0.f};
-#pragma unroll
-    for (int k = 0; k < kNv; ++k)
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const float c = x[k][i] - mean;
-            if (column<kVec>(k, i, t, T) < dim) q[0] = fmaf(c, c, q[0]);
+            for (int i = 0; i < kV / 2; ++i) {
+                const float2 c = there<kVec>(add2(x[k].pair(i), nm), k, i, t, T, dim);
+                q = fma2(c, c, q);
+            }
+        float v[1] = {q.x + q.y};
+        row_sum<1>(v, T, group, red[buf][1]);
+        const float rstd = rsqrtf(fmaf(v[0], p.inv_dim, p.eps));
+        if (t == 0) {
+            if (p.mean && !p.rms) p.mean[row] = -nm.x;
+            if (p.rstd) p.rstd[row] = rstd;
         }
-    row_sum<1>(q, T, group, red[1]);
-    const float rstd = rsqrtf(fmaf(q[0], p.inv_dim, p.eps));
-    if (t == 0) {
-        if (p.mean && !p.rms) p.mean[row] = mean;
-        if (p.rstd) p.rstd[row] = rstd;
-    }
-    Tout *y = static_cast<Tout *>(p.y) + row * p.dim;
+        Tout *y = static_cast<Tout *>(p.y) + row * p.dim;
 #pragma unroll
-    for (int k = 0; k < kNv; ++k) {
-        float w[kV], b[kV], v[kV];
-        load_cols<kVec>(w, p.weight, k, t, T, dim, 1.f);
-        load_cols<kVec>(b, p.bias, k, t, T, dim, 0.f);
+        for (int k = 0; k < kNv; ++k) {
+            float o[kV];
 #pragma unroll
-        for (int i = 0; i < kV; ++i) v[i] = fmaf((x[k][i] - mean) * rstd, w[i], b[i]);
-        store_cols<Tout, kVec>(y, v, k, t, T, dim);
+            for (int i = 0; i < kV / 2; ++i) {
+                const float2 r = fma2(mul2(add2(x[k].pair(i), nm), both(rstd)), w[k][i], b[k][i]);
+                o[2 * i] = r.x, o[2 * i + 1] = r.y;
+            }
+            store_cols<Tout, kVec>(y, o, k, t, T, dim);
+        }
     }
 }
 
@@ -209,82 +238,81 @@ __global__ void __launch_bounds__(1024) norm_rows_fwd_wide_kernel(const NormPara
         put(y, c, fmaf((load_elem(x, c) - mean) * rstd, p.weight ? __ldg(p.weight + c) : 1.f, p.bias ? __ldg(p.bias + c) : 0.f));
 }
 
+// Blocks stay and walk over the rows.  A thread's columns are the same in
+// every row, so their parts of dw and db are sums in its registers, joined
+// over the block's groups at the end.
 template <typename Tin, typename Tout, int kNv, bool kVec>
 __global__ void __launch_bounds__(512) norm_rows_bwd_kernel(const NormParams p, int T) {
-    extern __shared__ float acc[];  // the groups' sums, joined at the end
+    extern __shared__ float acc[];  // groups x 2 x dim
     __shared__ float red[2][16][2];
-    const int groups = blockDim.x / T, group = threadIdx.x / T, t = threadIdx.x - group * T;
-    const int dim = (int)p.dim;
+    const int groups = blockDim.x / T, group = threadIdx.x / T, t = threadIdx.x - group * T, dim = (int)p.dim;
     const int64_t step = (int64_t)gridDim.x * groups;
-    float dw[kNv][kV], db[kNv][kV];
+    float2 dw[kNv][kV / 2], db[kNv][kV / 2], w[kNv][kV / 2];
 #pragma unroll
-    for (int k = 0; k < kNv; ++k)
+    for (int k = 0; k < kNv; ++k) {
+        load_cols<kVec>(w[k], p.weight, k, t, T, dim, 1.f);
 #pragma unroll
-        for (int i = 0; i < kV; ++i) dw[k][i] = db[k][i] = 0.f;
+        for (int i = 0; i < kV / 2; ++i) dw[k][i] = db[k][i] = both(0.f);
+    }
     int buf = 0;
     for (int64_t row = (int64_t)blockIdx.x * groups + group; row < p.batch; row += step, buf ^= 1) {
         Vec8<Tin> x[kNv];
         Vec8<Tout> dy[kNv];
         load_row<Tin, kNv, kVec>(x, static_cast<const Tin *>(p.x) + row * p.dim, t, T, dim);
         load_row<Tout, kNv, kVec>(dy, static_cast<const Tout *>(p.dy) + row * p.dim, t, T, dim);
-        const float mean = p.mean_in ? __ldg(p.mean_in + row) : 0.f, rstd = __ldg(p.rstd_in + row);
-        float c[2] = {0.f, 0.f};
+        const float2 nm = both(p.mean_in ? -__ldg(p.mean_in + row) : 0.f);
+        const float rstd = __ldg(p.rstd_in + row);
+        // elements that are not there have dy = 0, and count in no sum
+        float2 c1 = both(0.f), c2 = both(0.f);
 #pragma unroll
-        for (int k = 0; k < kNv; ++k) {
-            float w[kV];
-            load_cols<kVec>(w, p.weight, k, t, T, dim, 1.f);
+        for (int k = 0; k < kNv; ++k)
 #pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                if (column<kVec>(k, i, t, T) < dim) {
-                    const float g = dy[k][i], xh = (x[k][i] - mean) * rstd, v = g * w[i];
-                    c[0] += v;
-                    c[1] = fmaf(v, xh, c[1]);
-                    dw[k][i] = fmaf(g, xh, dw[k][i]);
-                    db[k][i] += g;
-                }
+            for (int i = 0; i < kV / 2; ++i) {
+                const float2 g = dy[k].pair(i), h = mul2(g, mul2(add2(x[k].pair(i), nm), both(rstd)));
+                c1 = fma2(g, w[k][i], c1);
+                c2 = fma2(h, w[k][i], c2);
+                dw[k][i] = add2(dw[k][i], h);
+                db[k][i] = add2(db[k][i], g);
             }
-        }
+        float c[2] = {c1.x + c1.y, c2.x + c2.y};
         row_sum<2>(c, T, group, red[buf]);
 #pragma unroll
         for (int k = 0; k < kNv; ++k) x[k].again(), dy[k].again();
-        const float c1 = p.mean_in ? c[0] * p.inv_dim : 0.f, c2 = c[1] * p.inv_dim;
+        // dx = rstd v - rstd c1 - (x - m) rstd^2 c2
+        const float f = -rstd * p.inv_dim;
+        const float2 a1 = both(p.mean_in ? c[0] * f : 0.f), a2 = both(c[1] * f * rstd);
         Tin *dx = static_cast<Tin *>(p.dx) + row * p.dim;
 #pragma unroll
         for (int k = 0; k < kNv; ++k) {
-            float w[kV], v[kV];
-            load_cols<kVec>(w, p.weight, k, t, T, dim, 1.f);
+            float o[kV];
 #pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                const float xh = (x[k][i] - mean) * rstd;
-                v[i] = (fmaf(dy[k][i], w[i], -c1) - xh * c2) * rstd;
+            for (int i = 0; i < kV / 2; ++i) {
+                const float2 r = fma2(add2(x[k].pair(i), nm), a2, fma2(mul2(dy[k].pair(i), w[k][i]), both(rstd), a1));
+                o[2 * i] = r.x, o[2 * i + 1] = r.y;
             }
-            store_cols<Tin, kVec>(dx, v, k, t, T, dim);
+            store_cols<Tin, kVec>(dx, o, k, t, T, dim);
         }
     }
     if (!p.sums) return;
     float *out = p.part + (int64_t)blockIdx.x * 2 * p.dim;
-    if (groups > 1) {  // the same columns, one group after the other
-        for (int g = 0; g < groups; ++g) {
-            if (group == g) {
+    float *to = groups > 1 ? acc + group * 2 * dim : out;
 #pragma unroll
-                for (int k = 0; k < kNv; ++k)
+    for (int k = 0; k < kNv; ++k) {
+        float o[kV], u[kV];
 #pragma unroll
-                    for (int i = 0; i < kV; ++i) {
-                        const int c = column<kVec>(k, i, t, T);
-                        if (c < dim) {
-                            acc[c] = g ? acc[c] + dw[k][i] : dw[k][i];
-                            acc[dim + c] = g ? acc[dim + c] + db[k][i] : db[k][i];
-                        }
-                    }
-            }
-            __syncthreads();
+        for (int i = 0; i < kV / 2; ++i) {
+            o[2 * i] = dw[k][i].x, o[2 * i + 1] = dw[k][i].y;
+            u[2 * i] = db[k][i].x, u[2 * i + 1] = db[k][i].y;
         }
-        for (int c = threadIdx.x; c < 2 * dim; c += blockDim.x) out[c] = acc[c];
-    } else {
-#pragma unroll
-        for (int k = 0; k < kNv; ++k) {
-            store_cols<float, kVec>(out, dw[k], k, t, T, dim);
-            store_cols<float, kVec>(out + dim, db[k], k, t, T, dim);
+        store_cols<float, kVec>(to, o, k, t, T, dim);
+        store_cols<float, kVec>(to + dim, u, k, t, T, dim);
+    }
+    if (groups > 1) {
+        __syncthreads();
+        for (int c = threadIdx.x; c < 2 * dim; c += blockDim.x) {
+            float v = 0.f;
+            for (int g = 0; g < groups; ++g) v += acc[g * 2 * dim + c];
+            out[c] = v;
         }
     }
 }
@@ -336,28 +364,61 @@ __device__ __forceinline__ void peer_store(float2 *p, int rank, float2 v) {
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(peer), "f"(v.x), "f"(v.y) : "memory");
 }
 
-// V consecutive steps of a channel as they lie in memory: one or two 16-byte
-// words, or a single element.
+// How a warp covers its 32 channels: kLs lanes along the steps, V steps each
+// (16 bytes of the input), and kLc lanes by kN channels.  V = 1 where rows
+// are not whole vectors: then every lane has a step and all 32 channels.
+// A thread's elements are worked in pairs, with the packed arithmetic of two
+// floats: neighbouring steps of a channel, or with V = 1 neighbouring
+// channels.  Pair q belongs to channel chan(q) (and the next one with V = 1)
+// and to the statistics stat(q).
+template <int V>
+struct Tile {
+    static constexpr int kLc = V == 1 ? 1 : 4, kLs = 32 / kLc, kN = kWarpCh / kLc, kSteps = kLs * V;
+    static constexpr int kPairs = kN * V / 2, kStats = V == 1 ? 1 : V / 2;
+    __device__ static constexpr int chan(int q) { return V == 1 ? 2 * q : q / kStats; }
+    __device__ static constexpr int stat(int q) { return V == 1 ? 0 : q % kStats; }
+};
+
+// A thread's elements as they lie in memory.
 template <typename T, int V>
-struct Run {
-    static constexpr int kWords = V * sizeof(T) >= 4 ? V * sizeof(T) / 4 : 1;
+struct Patch {
+    using G = Tile<V>;
+    static constexpr int kWords = G::kPairs * sizeof(T) / 2;
     uint32_t w[kWords];
-    __device__ __forceinline__ float operator[](int i) const { return Io<T>::widen(w, i); }
-    __device__ __forceinline__ void load(const T *p) {
+    __device__ __forceinline__ float2 pair(int q) const { return pair_of<T>(w, q); }
+    // Channels 0 .. kN-1, `apart` elements from one to the next; those from
+    // `have` on are read from the last one there is, and cleared.
+    __device__ __forceinline__ void load(const T *p, int64_t apart, int have) {
         if constexpr (V == 1) {
-            w[0] = Io<T>::bits(p, 0);
-        } else {
-            const uint4 *q = reinterpret_cast<const uint4 *>(p);
+            uint32_t b[G::kN];
 #pragma unroll
-            for (int k = 0; k < kWords / 4; ++k) {
-                const uint4 u = __ldg(q + k);
-                w[4 * k] = u.x, w[4 * k + 1] = u.y, w[4 * k + 2] = u.z, w[4 * k + 3] = u.w;
+            for (int i = 0; i < G::kN; ++i) b[i] = Io<T>::bits(p + min(i, max(have - 1, 0)) * apart, 0);
+#pragma unroll
+            for (int i = 0; i < G::kN; ++i) {
+                if constexpr (sizeof(T) == 4) w[i] = b[i];
+                else if (i % 2) w[i / 2] = __byte_perm(b[i - 1], b[i], 0x5410);
+            }
+        } else {
+            constexpr int kQ = V * sizeof(T) / 16;
+#pragma unroll
+            for (int i = 0; i < G::kN; ++i) {
+                const uint4 *q = reinterpret_cast<const uint4 *>(p + min(i, max(have - 1, 0)) * apart);
+#pragma unroll
+                for (int k = 0; k < kQ; ++k) {
+                    const uint4 u = __ldg(q + k);
+                    uint32_t *v = w + (i * kQ + k) * 4;
+                    v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+                }
             }
         }
     }
-    __device__ __forceinline__ void clear() {
+    __device__ __forceinline__ void keep(int have) {  // clears the channels from `have` on
+        if (have >= G::kN) return;
 #pragma unroll
-        for (int k = 0; k < kWords; ++k) w[k] = 0u;
+        for (int k = 0; k < kWords; ++k) {
+            if (V == 1 && sizeof(T) == 2) w[k] &= 2 * k + 1 < have ? ~0u : 2 * k < have ? 0xffffu : 0u;
+            else if (k * G::kN / kWords >= have) w[k] = 0u;
+        }
     }
     __device__ __forceinline__ void again() {  // as Vec8::again
 #pragma unroll
@@ -365,29 +426,36 @@ struct Run {
     }
 };
 
+// The pairs of channel i (with V = 1: i and i + 1) to p.
 template <int V>
-__device__ __forceinline__ void store_run_of(float *p, const float (&v)[V]) {
+__device__ __forceinline__ void store_pairs(float *p, int64_t apart, const float2 *v, bool second) {
     if constexpr (V == 1) {
-        *p = v[0];
+        p[0] = v[0].x;
+        if (second) p[apart] = v[0].y;
     } else {
 #pragma unroll
         for (int k = 0; k < V / 4; ++k)
-            reinterpret_cast<float4 *>(p)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            reinterpret_cast<float4 *>(p)[k] = make_float4(v[2 * k].x, v[2 * k].y, v[2 * k + 1].x, v[2 * k + 1].y);
     }
 }
 template <int V>
-__device__ __forceinline__ void store_run_of(__nv_bfloat16 *p, const float (&v)[V]) {
-    if constexpr (V == 1) *p = __float2bfloat16_rn(v[0]);
-    else store_vec(p, v);
+__device__ __forceinline__ void store_pairs(__nv_bfloat16 *p, int64_t apart, const float2 *v, bool second) {
+    if constexpr (V == 1) {
+        p[0] = __float2bfloat16_rn(v[0].x);
+        if (second) p[apart] = __float2bfloat16_rn(v[0].y);
+    } else {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                                   pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+    }
 }
 
-// How a warp covers its 32 channels: kLs lanes along the steps, V steps each
-// (16 bytes of the input), and kLc lanes by kN channels.  V = 1 where rows
-// are not whole vectors: then every lane has a step and all 32 channels.
+// A per-channel parameter for the pairs of channel c0 + i kLc (null: `none`).
 template <int V>
-struct Tile {
-    static constexpr int kLc = V == 1 ? 1 : 4, kLs = 32 / kLc, kN = kWarpCh / kLc, kSteps = kLs * V;
-};
+__device__ __forceinline__ float2 param(const float *p, int64_t c, bool second, float none) {
+    if (!p) return both(none);
+    const float v = __ldg(p + c);
+    return V == 1 ? make_float2(v, __ldg(p + c + (second ? 1 : 0))) : both(v);
+}
 
 // Where a lane's steps lie: element of channel 0, index among all steps (the
 // last ones again for a lane behind the end).
@@ -415,108 +483,127 @@ __device__ __forceinline__ int have_of(const NormParams &p, int64_t c0) {
     return c0 >= p.dim ? 0 : (int)min((int64_t)G::kN, (p.dim - c0 + G::kLc - 1) / G::kLc);
 }
 
-// Makes a distance opaque: addresses are computed anew from here, rather than
-// kept in registers since the loads.
+// Makes a value opaque: what depends on it is computed anew from here, rather
+// than kept in registers.
 __device__ __forceinline__ void again(int64_t &v) { asm volatile("" : "+l"(v)); }
 
-// (n, m, S) and (nb, mb, Sb), number, mean and squares about the mean, into
-// one: m + (mb - m) nb / (n + nb), S + Sb + (mb - m)^2 n nb / (n + nb).
-__device__ __forceinline__ void join(float f, float h, float &m, float &S, float mb, float Sb) {
-    const float d = mb - m;
-    m = fmaf(d, f, m);
-    S += fmaf(d * d, h, Sb);
+// Sums over the kLc lanes that share a step, and over a pair with V = 1.
+template <int V>
+__device__ __forceinline__ void lanes_sum(float2 (&v)[Tile<V>::kStats]) {
+    if constexpr (V == 1) {
+        v[0] = both(v[0].x + v[0].y);
+    } else {
+#pragma unroll
+        for (int o = Tile<V>::kLs; o < 32; o *= 2)
+#pragma unroll
+            for (int k = 0; k < Tile<V>::kStats; ++k)
+                v[k] = add2(v[k], make_float2(__shfl_xor_sync(0xffffffffu, v[k].x, o), __shfl_xor_sync(0xffffffffu, v[k].y, o)));
+    }
 }
 
-// Forward over steps.  The statistics of a step come together in four
+// Means and squares about them of kMost parts or fewer, of n(k) channels each,
+// into those of all:  m = sum n m_k / sum n,  S = sum S_k + n (m_k - m)^2.
+template <int kMost, typename N>
+__device__ __forceinline__ float2 join(const float2 *part, int stride, int parts, N n) {
+    float2 v[kMost];
+    float all = 0.f, m = 0.f, S = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMost; ++k)
+        if (k < parts) {
+            v[k] = part[k * stride];
+            m = fmaf(n(k), v[k].x, m);
+            all += n(k);
+        }
+    m = all > 0.f ? m / all : 0.f;
+#pragma unroll
+    for (int k = 0; k < kMost; ++k)
+        if (k < parts) {
+            const float d = v[k].x - m;
+            S += fmaf(n(k) * d, d, v[k].y);
+        }
+    return make_float2(m, S);
+}
+
+// Forward over steps.  The statistics of a step come together in three
 // stages, always as mean and squares about it (no difference of large sums):
-// a thread's channels, the kLc lanes, the block's warps, the cluster's
-// blocks; each block writes its own into every other's shared memory, so one
-// cluster barrier is all they wait for.
+// a warp's channels, the block's warps, the cluster's blocks; each block
+// writes its own into every other's shared memory, so one cluster barrier is
+// all they wait for.
 template <typename Tin, typename Tout, int V, int kMaxW>
 __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 3 : 1) norm_steps_fwd_kernel(const NormParams p, int nblk) {
     using G = Tile<V>;
-    __shared__ float2 part[kMaxW][G::kSteps], slot[8][G::kSteps], stat[G::kSteps];
+    __shared__ float2 part[kMaxW][G::kSteps], slot[8][G::kSteps];
+    __shared__ __align__(16) float stat[2][G::kSteps];  // -mean, 1 / deviation
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int rank = (int)(blockIdx.x % nblk), sl = lane % G::kLs, cl = lane / G::kLs;
     if (nblk > 1) cluster_arrive();  // waited for before the first remote store
-    const int64_t c0 = ((int64_t)rank * warps + warp) * kWarpCh + cl;  // channels c0 + i kLc
+    const int64_t w0 = ((int64_t)rank * warps + warp) * kWarpCh, c0 = w0 + cl;  // channels c0 + i kLc
     const Place at = place_of<V>(p, blockIdx.x / nblk, sl);
     const int have = have_of<V>(p, c0);
     const int64_t first = at.at + min(c0, p.dim - 1) * p.L;
-    const Tin *x = static_cast<const Tin *>(p.x) + first;
     int64_t apart = G::kLc * p.L;
-    Run<Tin, V> r[G::kN];
-#pragma unroll
-    for (int i = 0; i < G::kN; ++i) r[i].load(x + min(i, max(have - 1, 0)) * apart);
+    Patch<Tin, V> x;
+    x.load(static_cast<const Tin *>(p.x) + first, apart, have);
+    x.keep(have);
 
-    float m[V], S[V];
-    const float n0 = (float)have, inv0 = have ? 1.f / n0 : 0.f;
+    float2 nm[G::kStats], S[G::kStats];
 #pragma unroll
-    for (int j = 0; j < V; ++j) m[j] = S[j] = 0.f;
-    if (!p.rms) {
+    for (int k = 0; k < G::kStats; ++k) nm[k] = S[k] = both(0.f);
+    const float nw = clamp_count(p.dim - w0, kWarpCh);
+    if (!p.rms && nw > 0.f) {
 #pragma unroll
-        for (int i = 0; i < G::kN; ++i)
+        for (int q = 0; q < G::kPairs; ++q) nm[G::stat(q)] = add2(nm[G::stat(q)], x.pair(q));
+        lanes_sum<V>(nm);
+        const float2 f = both(-1.f / nw);
 #pragma unroll
-            for (int j = 0; j < V; ++j) m[j] += i < have ? r[i][j] : 0.f;
-#pragma unroll
-        for (int j = 0; j < V; ++j) m[j] *= inv0;
+        for (int k = 0; k < G::kStats; ++k) nm[k] = mul2(nm[k], f);
     }
+    if (nw == kWarpCh) {
 #pragma unroll
-    for (int i = 0; i < G::kN; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float c = i < have ? r[i][j] - m[j] : 0.f;
-            S[j] = fmaf(c, c, S[j]);
+        for (int q = 0; q < G::kPairs; ++q) {
+            const float2 d = add2(x.pair(q), nm[G::stat(q)]);
+            S[G::stat(q)] = fma2(d, d, S[G::stat(q)]);
         }
-    float n = n0;
+    } else {
 #pragma unroll
-    for (int o = G::kLs; o < 32; o *= 2) {
-        const float nb = __shfl_xor_sync(0xffffffffu, n, o), both = n + nb;
-        const float f = both > 0.f ? nb / both : 0.f, h = n * f;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float mb = __shfl_xor_sync(0xffffffffu, m[j], o), Sb = __shfl_xor_sync(0xffffffffu, S[j], o);
-            join(f, h, m[j], S[j], mb, Sb);
+        for (int q = 0; q < G::kPairs; ++q) {
+            float2 d = add2(x.pair(q), nm[G::stat(q)]);
+            if (G::chan(q) >= have) d = both(0.f);
+            if (V == 1 && G::chan(q) + 1 >= have) d.y = 0.f;
+            S[G::stat(q)] = fma2(d, d, S[G::stat(q)]);
         }
-        n = both;
     }
+    lanes_sum<V>(S);
     if (cl == 0) {
+        if constexpr (V == 1) {
+            part[warp][sl] = make_float2(-nm[0].x, S[0].x);
+        } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) part[warp][sl * V + j] = make_float2(m[j], S[j]);
+            for (int k = 0; k < G::kStats; ++k) {
+                part[warp][sl * V + 2 * k] = make_float2(-nm[k].x, S[k].x);
+                part[warp][sl * V + 2 * k + 1] = make_float2(-nm[k].y, S[k].y);
+            }
+        }
     }
     __syncthreads();
     const int t = threadIdx.x;
     const int64_t wide = (int64_t)warps * kWarpCh;
     float2 all = make_float2(0.f, 0.f);
-    if (t < G::kSteps) {
-        float nn = 0.f;
-        for (int k = 0; k < warps; ++k) {
-            const float nk = clamp_count(p.dim - (rank * wide + k * kWarpCh), kWarpCh), both = nn + nk;
-            const float f = both > 0.f ? nk / both : 0.f;
-            join(f, nn * f, all.x, all.y, part[k][t].x, part[k][t].y);
-            nn = both;
-        }
-    }
+    if (t < G::kSteps)
+        all = join<kMaxW>(&part[0][t], G::kSteps, warps,
+                          [&](int k) { return clamp_count(p.dim - (rank * wide + k * kWarpCh), kWarpCh); });
     if (nblk > 1) {
         cluster_wait();  // every block has begun
         if (t < G::kSteps)
             for (int k = 0; k < nblk; ++k) peer_store(&slot[rank][t], k, all);
         cluster_arrive();
         cluster_wait();
-        if (t < G::kSteps) {
-            float nn = 0.f;
-            all = make_float2(0.f, 0.f);
-            for (int k = 0; k < nblk; ++k) {
-                const float nk = clamp_count(p.dim - k * wide, wide), both = nn + nk;
-                const float f = both > 0.f ? nk / both : 0.f;
-                join(f, nn * f, all.x, all.y, slot[k][t].x, slot[k][t].y);
-                nn = both;
-            }
-        }
+        if (t < G::kSteps)
+            all = join<8>(&slot[0][t], G::kSteps, nblk, [&](int k) { return clamp_count(p.dim - k * wide, wide); });
     }
     if (t < G::kSteps) {
         const float rstd = rsqrtf(fmaf(all.y, p.inv_dim, p.eps));
-        stat[t] = make_float2(all.x, rstd);
+        stat[0][t] = -all.x, stat[1][t] = rstd;
         const int64_t s = (blockIdx.x / nblk) * (int64_t)G::kSteps + t;
         if (rank == 0 && s < p.batch * p.L) {
             if (p.mean && !p.rms) p.mean[s] = all.x;
@@ -525,25 +612,28 @@ __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 3 : 1) norm_steps_fwd
     }
     __syncthreads();
     if (!at.in) return;
+    x.again(), again(apart);
 #pragma unroll
-    for (int i = 0; i < G::kN; ++i) r[i].again();
-    float rstd[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const float2 q = stat[sl * V + j];
-        m[j] = q.x, rstd[j] = q.y;
+    for (int k = 0; k < G::kStats; ++k) {
+        if constexpr (V == 1) {
+            nm[0] = both(stat[0][sl]), S[0] = both(stat[1][sl]);
+        } else {
+            nm[k] = *reinterpret_cast<const float2 *>(&stat[0][sl * V + 2 * k]);
+            S[k] = *reinterpret_cast<const float2 *>(&stat[1][sl * V + 2 * k]);
+        }
     }
     Tout *y = static_cast<Tout *>(p.y) + first;
-    again(apart);
+    constexpr int kRun = V == 1 ? 1 : V / 2;  // pairs stored together
 #pragma unroll
-    for (int i = 0; i < G::kN; ++i) {
+    for (int q = 0; q < G::kPairs; q += kRun) {
+        const int i = G::chan(q);
         if (i < have) {
-            const int64_t c = c0 + i * G::kLc;
-            const float w = p.weight ? __ldg(p.weight + c) : 1.f, b = p.bias ? __ldg(p.bias + c) : 0.f;
-            float v[V];
+            const bool second = V == 1 && i + 1 < have;
+            const float2 w = param<V>(p.weight, c0 + i * G::kLc, second, 1.f), b = param<V>(p.bias, c0 + i * G::kLc, second, 0.f);
+            float2 v[kRun];
 #pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = fmaf((r[i][j] - m[j]) * rstd[j], w, b);
-            store_run_of<V>(y + i * apart, v);
+            for (int k = 0; k < kRun; ++k) v[k] = fma2(mul2(add2(x.pair(q + k), nm[k]), S[k]), w, b);
+            store_pairs<V>(y + i * apart, apart, v, second);
         }
     }
 }
@@ -576,6 +666,7 @@ __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 2 : 1) norm_steps_bwd
     const int64_t c0 = ((int64_t)rank * warps + warp) * kWarpCh + cl;
     const int have = have_of<V>(p, c0);
     const int64_t tiles = (p.batch * p.L + G::kSteps - 1) / G::kSteps;
+    constexpr int kRun = V == 1 ? 1 : V / 2;
     if (nblk > 1) cluster_arrive();
     bool begun = nblk == 1;
     float dw = 0.f, db = 0.f;  // of channel c0 + sl kLc
@@ -583,70 +674,58 @@ __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 2 : 1) norm_steps_bwd
     for (int64_t tile = group; tile < tiles; tile += groups, buf ^= 1) {
         const Place at = place_of<V>(p, tile, sl);
         const int64_t first = at.at + min(c0, p.dim - 1) * p.L;
-        const Tin *x = static_cast<const Tin *>(p.x) + first;
-        const Tout *dy = static_cast<const Tout *>(p.dy) + first;
-        int64_t apart = G::kLc * p.L, wc = c0;  // (made opaque: not kept in registers from tile to tile)
-        again(apart), again(wc);
-        Run<Tin, V> rx[G::kN];
-        Run<Tout, V> rg[G::kN];
+        int64_t apart = G::kLc * p.L, wc = c0;
+        again(apart), again(wc);  // nothing of them is kept from tile to tile
+        Patch<Tin, V> x;
+        Patch<Tout, V> g;
+        x.load(static_cast<const Tin *>(p.x) + first, apart, have);
+        g.load(static_cast<const Tout *>(p.dy) + first, apart, have);
+        float2 nm[G::kStats], r[G::kStats], s1[G::kStats], s2[G::kStats];
 #pragma unroll
-        for (int i = 0; i < G::kN; ++i) {
-            const int64_t c = min(i, max(have - 1, 0)) * apart;
-            rx[i].load(x + c);
-            rg[i].load(dy + c);
+        for (int k = 0; k < G::kStats; ++k) {
+            const int64_t s = at.index + 2 * k;
+            constexpr int kNext = V == 1 ? 0 : 1;
+            nm[k] = p.mean_in ? make_float2(-__ldg(p.mean_in + s), -__ldg(p.mean_in + s + kNext)) : both(0.f);
+            r[k] = make_float2(__ldg(p.rstd_in + s), __ldg(p.rstd_in + s + kNext));
+            s1[k] = s2[k] = both(0.f);
         }
-        float m[V], rstd[V], s1[V], s2[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            m[j] = p.mean_in ? __ldg(p.mean_in + at.index + j) : 0.f;
-            rstd[j] = __ldg(p.rstd_in + at.index + j);
-            s1[j] = s2[j] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < G::kN; ++i) {
-            if (i >= have) rx[i].clear();
-            if (i >= have || !at.in) rg[i].clear();
-        }
+        x.keep(have);
+        g.keep(at.in ? have : 0);
         float term[G::kN];
 #pragma unroll
-        for (int i = 0; i < G::kN; ++i) {
-            const float w = p.weight ? __ldg(p.weight + min(wc + i * G::kLc, p.dim - 1)) : 1.f;
-            term[i] = 0.f;
+        for (int q = 0; q < G::kPairs; q += kRun) {
+            const int i = G::chan(q);
+            const bool second = V == 1 && i + 1 < have;
+            const float2 w = param<V>(p.weight, i < have ? wc + i * G::kLc : min(c0, p.dim - 1), second, 1.f);
+            float2 sum = both(0.f);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float g = rg[i][j], xh = (rx[i][j] - m[j]) * rstd[j], t = g * xh;
-                s1[j] = fmaf(g, w, s1[j]);
-                s2[j] = fmaf(t, w, s2[j]);
-                term[i] += t;
+            for (int k = 0; k < kRun; ++k) {
+                const float2 gv = g.pair(q + k), t = mul2(gv, mul2(add2(x.pair(q + k), nm[k]), r[k]));
+                s1[k] = fma2(gv, w, s1[k]);
+                s2[k] = fma2(t, w, s2[k]);
+                sum = add2(sum, t);
             }
+            if constexpr (V == 1) term[i] = sum.x, term[i + 1] = sum.y;
+            else term[i] = sum.x + sum.y;
         }
-        if (p.sums) {
-            dw += lane_sums<G::kN>(term, lane);
-#pragma unroll
-            for (int i = 0; i < G::kN; ++i) {
-                term[i] = rg[i][0];
-#pragma unroll
-                for (int j = 1; j < V; ++j) term[i] += rg[i][j];
-            }
-            db += lane_sums<G::kN>(term, lane);
-        }
-#pragma unroll
-        for (int o = G::kLs; o < 32; o *= 2) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                s1[j] += __shfl_xor_sync(0xffffffffu, s1[j], o);
-                s2[j] += __shfl_xor_sync(0xffffffffu, s2[j], o);
-            }
-        }
+        if (p.sums) dw += lane_sums<G::kN>(term, lane);
+        lanes_sum<V>(s1), lanes_sum<V>(s2);
         if (cl == 0) {
+            if constexpr (V == 1) {
+                part[warp][sl] = make_float2(s1[0].x, s2[0].x);
+            } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) part[warp][sl * V + j] = make_float2(s1[j], s2[j]);
+                for (int k = 0; k < G::kStats; ++k) {
+                    part[warp][sl * V + 2 * k] = make_float2(s1[k].x, s2[k].x);
+                    part[warp][sl * V + 2 * k + 1] = make_float2(s1[k].y, s2[k].y);
+                }
+            }
         }
         __syncthreads();
         const int t = threadIdx.x;
         float2 all = make_float2(0.f, 0.f);
         if (t < G::kSteps)
-            for (int k = 0; k < warps; ++k) all.x += part[k][t].x, all.y += part[k][t].y;
+            for (int k = 0; k < warps; ++k) all = add2(all, part[k][t]);
         if (nblk > 1) {
             if (!begun) cluster_wait();  // every block has begun
             begun = true;
@@ -661,35 +740,39 @@ __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 2 : 1) norm_steps_bwd
             if (t < G::kSteps) slot[buf][0][t] = all;
             __syncthreads();
         }
+        x.again(), g.again(), again(apart), again(wc);
+        // dx = rstd v - rstd c1 - (x - m) rstd^2 c2, with the step's factors
+        // made once; s1, s2: -rstd c1, -rstd^2 c2
 #pragma unroll
-        for (int i = 0; i < G::kN; ++i) rx[i].again(), rg[i].again();
-        if (at.in) {
-            // dx = rstd v - rstd c1 - (x - m) rstd^2 c2, with the step's
-            // factors made once
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float2 c = make_float2(0.f, 0.f);
-                for (int k = 0; k < nblk; ++k) {
-                    const float2 q = slot[buf][k][sl * V + j];
-                    c.x += q.x, c.y += q.y;
-                }
-                s1[j] = p.mean_in ? c.x * p.inv_dim * rstd[j] : 0.f;
-                s2[j] = c.y * p.inv_dim * rstd[j] * rstd[j];
+        for (int k = 0; k < G::kStats; ++k) {
+            float2 c = both(0.f), d = both(0.f);  // the sums of both steps of the pair
+            for (int b = 0; b < nblk; ++b) {
+                c = add2(c, slot[buf][b][V == 1 ? sl : sl * V + 2 * k]);
+                if (V > 1) d = add2(d, slot[buf][b][sl * V + 2 * k + (V > 1)]);
             }
-            Tin *dx = static_cast<Tin *>(p.dx) + first;
-            again(apart), again(wc);
-#pragma unroll
-            for (int i = 0; i < G::kN; ++i) {
-                if (i < have) {
-                    const float w = p.weight ? __ldg(p.weight + wc + i * G::kLc) : 1.f;
-                    float v[V];
-#pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        v[j] = fmaf(rg[i][j] * w, rstd[j], -s1[j]) - (rx[i][j] - m[j]) * s2[j];
-                    store_run_of<V>(dx + i * apart, v);
-                }
-            }
+            if (V == 1) d = c;
+            const float2 f = mul2(r[k], both(-p.inv_dim));
+            s1[k] = p.mean_in ? mul2(make_float2(c.x, d.x), f) : both(0.f);
+            s2[k] = mul2(mul2(make_float2(c.y, d.y), f), r[k]);
         }
+        Tin *dx = static_cast<Tin *>(p.dx) + first;
+#pragma unroll
+        for (int q = 0; q < G::kPairs; q += kRun) {
+            const int i = G::chan(q);
+            const bool second = V == 1 && i + 1 < have;
+            const float2 w = param<V>(p.weight, i < have ? wc + i * G::kLc : min(c0, p.dim - 1), second, 1.f);
+            float2 v[kRun], sum = both(0.f);
+#pragma unroll
+            for (int k = 0; k < kRun; ++k) {
+                const float2 gv = g.pair(q + k);
+                sum = add2(sum, gv);
+                v[k] = fma2(add2(x.pair(q + k), nm[k]), s2[k], fma2(mul2(gv, w), r[k], s1[k]));
+            }
+            if (i < have && at.in) store_pairs<V>(dx + i * apart, apart, v, second);
+            if constexpr (V == 1) term[i] = sum.x, term[i + 1] = sum.y;
+            else term[i] = sum.x + sum.y;
+        }
+        if (p.sums) db += lane_sums<G::kN>(term, lane);
     }
     if (p.sums && sl < have) {
         float *out = p.part + group * 2 * p.dim;
@@ -821,9 +904,10 @@ NormPlan norm_plan(const ss_desc *desc, bool vec) {
     const int64_t sms = layer_sm_count();
     pl.rows = desc->seqlen == 1;
     if (pl.rows) {
-        // The fewest threads that hold a row with four vectors each at most
-        // (two where elements are loaded one by one and cost more registers).
-        const int64_t vecs = (desc->dim + kV - 1) / kV, most = vec ? 4 : 2;
+        // The fewest threads that hold a row with three vectors each at most
+        // (two where elements are loaded one by one and cost more registers):
+        // the backward's sums, parameters and inputs then stay in 128 registers.
+        const int64_t vecs = (desc->dim + kV - 1) / kV, most = vec ? 3 : 2;
         pl.T = 32;
         while (pl.T < 512 && vecs > (int64_t)pl.T * most) pl.T *= 2;
         pl.nv = (int)((vecs + pl.T - 1) / pl.T);
@@ -878,11 +962,15 @@ template <typename Tin, typename Tout, int kNv, bool kVec>
 cudaError_t launch_rows(bool back, const NormPlan &pl, cudaStream_t s, const NormParams &p) {
     const int threads = pl.T * pl.per;
     if (back) {
-        const size_t smem = pl.per > 1 ? (size_t)p.dim * 2 * sizeof(float) : 0;  // at most 32 KB (T = 128)
+        const size_t smem = pl.per > 1 ? (size_t)pl.per * p.dim * 2 * sizeof(float) : 0;  // 48 KB at most: 256 threads of 24 columns
+        if (smem > 40 * 1024) {  // more than the default leaves beside the kernel's own
+            const cudaError_t e = cudaFuncSetAttribute(norm_rows_bwd_kernel<Tin, Tout, kNv, kVec>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+        }
         norm_rows_bwd_kernel<Tin, Tout, kNv, kVec><<<(unsigned)pl.parts, threads, smem, s>>>(p, pl.T);
     } else {
-        const int64_t grid = (p.batch + pl.per - 1) / pl.per;
-        norm_rows_fwd_kernel<Tin, Tout, kNv, kVec><<<(unsigned)grid, threads, 0, s>>>(p, pl.T);
+        norm_rows_fwd_kernel<Tin, Tout, kNv, kVec><<<(unsigned)pl.parts, threads, 0, s>>>(p, pl.T);
     }
     return cudaGetLastError();
 }
@@ -910,8 +998,7 @@ cudaError_t dispatch_norm(bool back, bool vec, const NormPlan &pl, cudaStream_t 
         switch (pl.nv) {
             case 1: return launch_rows<Tin, Tout, 1, true>(back, pl, s, p);
             case 2: return launch_rows<Tin, Tout, 2, true>(back, pl, s, p);
-            case 3: return launch_rows<Tin, Tout, 3, true>(back, pl, s, p);
-            default: return launch_rows<Tin, Tout, 4, true>(back, pl, s, p);
+            default: return launch_rows<Tin, Tout, 3, true>(back, pl, s, p);
         }
     }
     constexpr int kWhole = sizeof(Tin) == 2 ? 8 : 4;
