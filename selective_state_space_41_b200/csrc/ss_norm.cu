@@ -28,6 +28,8 @@
 // dw and db leave each block (or cluster) as one row of partial sums in the
 // workspace; a second kernel adds the rows in a fixed order, so the results
 // do not change from run to run.
+#include <type_traits>
+
 #include "ss_layer.cuh"
 
 namespace selscan {
@@ -501,26 +503,23 @@ __device__ __forceinline__ void lanes_sum(float2 (&v)[Tile<V>::kStats]) {
     }
 }
 
-// Means and squares about them of kMost parts or fewer, of n(k) channels each,
-// into those of all:  m = sum n m_k / sum n,  S = sum S_k + n (m_k - m)^2.
-template <int kMost, typename N>
+// Means and squares about them of parts of n(k) channels each into those of
+// all:  m = sum n m_k / sum n,  S = sum S_k + n (m_k - m)^2.
+template <typename N>
 __device__ __forceinline__ float2 join(const float2 *part, int stride, int parts, N n) {
-    float2 v[kMost];
     float all = 0.f, m = 0.f, S = 0.f;
-#pragma unroll
-    for (int k = 0; k < kMost; ++k)
-        if (k < parts) {
-            v[k] = part[k * stride];
-            m = fmaf(n(k), v[k].x, m);
-            all += n(k);
-        }
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+        m = fmaf(n(k), part[k * stride].x, m);
+        all += n(k);
+    }
     m = all > 0.f ? m / all : 0.f;
-#pragma unroll
-    for (int k = 0; k < kMost; ++k)
-        if (k < parts) {
-            const float d = v[k].x - m;
-            S += fmaf(n(k) * d, d, v[k].y);
-        }
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+        const float2 v = part[k * stride];
+        const float d = v.x - m;
+        S += fmaf(n(k) * d, d, v.y);
+    }
     return make_float2(m, S);
 }
 
@@ -590,7 +589,7 @@ __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 3 : 1) norm_steps_fwd
     const int64_t wide = (int64_t)warps * kWarpCh;
     float2 all = make_float2(0.f, 0.f);
     if (t < G::kSteps)
-        all = join<kMaxW>(&part[0][t], G::kSteps, warps,
+        all = join(&part[0][t], G::kSteps, warps,
                           [&](int k) { return clamp_count(p.dim - (rank * wide + k * kWarpCh), kWarpCh); });
     if (nblk > 1) {
         cluster_wait();  // every block has begun
@@ -599,7 +598,7 @@ __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 3 : 1) norm_steps_fwd
         cluster_arrive();
         cluster_wait();
         if (t < G::kSteps)
-            all = join<8>(&slot[0][t], G::kSteps, nblk, [&](int k) { return clamp_count(p.dim - k * wide, wide); });
+            all = join(&slot[0][t], G::kSteps, nblk, [&](int k) { return clamp_count(p.dim - k * wide, wide); });
     }
     if (t < G::kSteps) {
         const float rstd = rsqrtf(fmaf(all.y, p.inv_dim, p.eps));
@@ -781,6 +780,379 @@ __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 2 : 1) norm_steps_bwd
     }
 }
 
+// ---------------------------------------------------------- steps in shared memory
+//
+// Where rows are whole vectors and a tile of all channels fits into shared
+// memory, no cluster is needed: a block takes 64 bytes of every channel (32
+// steps of bf16, 16 of fp32), goes over them once for the statistics and once
+// for the results.  Every thread copies in the very units of 16 bytes that it
+// reads later, so the copies need no barrier, and as soon as it has read a
+// unit for the last time it starts the copy of the same unit of the block's
+// next tile: the loads of the next tile run under the results of this one.
+//
+// A warp covers 4 lanes along the steps by 8 channels; a batch is 4 of a
+// thread's units, as many as there are lanes along the steps, so that the
+// sums over the steps of a batch (backward) come out one unit to each lane.
+template <typename T>
+struct Geo {
+    static constexpr int kE = 16 / (int)sizeof(T), kLs = 4, kLc = 8, kB = 4, kSteps = kLs * kE;
+    static constexpr int kStats = kE / 2;  // pairs of a unit
+};
+
+template <typename T>
+struct Batch {
+    uint32_t w[4 * Geo<T>::kB];
+    __device__ __forceinline__ float2 pair(int j, int k) const { return pair_of<T>(w + 4 * j, k); }
+    __device__ __forceinline__ void read(const unsigned char *sm, int step) {  // units `step` bytes apart
+#pragma unroll
+        for (int j = 0; j < Geo<T>::kB; ++j) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(sm + j * step);
+            w[4 * j] = u.x, w[4 * j + 1] = u.y, w[4 * j + 2] = u.z, w[4 * j + 3] = u.w;
+        }
+    }
+};
+
+// p + j distances of `apart` bytes (32 bits: one multiply-add an address).
+template <typename T>
+__device__ __forceinline__ T *at_unit(T *p, uint32_t apart, int j) {
+    return reinterpret_cast<T *>(reinterpret_cast<uintptr_t>(p) + (uint64_t)apart * (uint32_t)j);
+}
+
+// Starts the copy of a batch of a tile, channels c, c + each, ... below dim
+// (kFull: all of them are); a lane without a step gets zeros.
+template <typename T, bool kFull>
+__device__ __forceinline__ void copy_batch(unsigned char *sm, int step, const T *src, uint32_t apart, int c, int each, int dim,
+                                           bool in) {
+#pragma unroll
+    for (int j = 0; j < Geo<T>::kB; ++j) {
+        if (kFull || c + j * each < dim) {
+            if (in) cp_async16(sm + j * step, at_unit(src, apart, j));
+            else *reinterpret_cast<uint4 *>(sm + j * step) = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ Place place_in(const NormParams &p, int64_t tile, int sl) {
+    using G = Geo<T>;
+    const int64_t s = tile * G::kSteps + sl * G::kE, n = p.batch * p.L;
+    Place r;
+    r.in = s < n;
+    r.index = r.in ? s : n - G::kE;
+    const int64_t b = n <= INT_MAX ? (int64_t)((uint32_t)r.index / (uint32_t)p.L) : r.index / p.L;
+    r.at = b * p.dim * p.L + (r.index - b * p.L);
+    return r;
+}
+
+template <int kN>
+__device__ __forceinline__ void store_unit(float *p, const float2 (&v)[kN]) {
+#pragma unroll
+    for (int k = 0; k < kN / 2; ++k)
+        reinterpret_cast<float4 *>(p)[k] = make_float4(v[2 * k].x, v[2 * k].y, v[2 * k + 1].x, v[2 * k + 1].y);
+}
+__device__ __forceinline__ void store_unit(__nv_bfloat16 *p, const float2 (&v)[4]) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                               pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+}
+
+// Sums over the 8 lanes of a warp that share a step.
+template <int kN>
+__device__ __forceinline__ void step_sums(float2 (&v)[kN]) {
+#pragma unroll
+    for (int o = 4; o < 32; o *= 2)
+#pragma unroll
+        for (int k = 0; k < kN; ++k)
+            v[k] = add2(v[k], make_float2(__shfl_xor_sync(0xffffffffu, v[k].x, o), __shfl_xor_sync(0xffffffffu, v[k].y, o)));
+}
+
+// A warp's statistics of its steps to a row of `to`.
+template <int kN>
+__device__ __forceinline__ void write_steps(float2 *to, int sl, const float2 (&a)[kN], const float2 (&b)[kN]) {
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+        to[(sl * kN + k) * 2] = make_float2(a[k].x, b[k].x);
+        to[(sl * kN + k) * 2 + 1] = make_float2(a[k].y, b[k].y);
+    }
+}
+
+template <int kN>
+__device__ __forceinline__ void read_steps(const float *from, int sl, float2 (&v)[kN]) {
+#pragma unroll
+    for (int k = 0; k < kN; ++k) v[k] = reinterpret_cast<const float2 *>(from)[sl * kN + k];
+}
+
+constexpr int kTileWarps = 16;  // of a block, at most
+
+// Calls f(batch, whole) for every batch; whole: every thread has all of its units.
+template <typename F>
+__device__ __forceinline__ void for_batches(int batches, int full, F f) {
+    int b = 0;
+    for (; b < full; ++b) f(b, std::true_type{});
+    for (; b < batches; ++b) f(b, std::false_type{});
+}
+
+// batches: a thread's units, in batches.  Shared memory: batches * 4 * T units.
+//
+// Statistics in one pass: differences d to a pivot, the mean of the thread's
+// first batch; then m = pivot + sum d / n and S = sum d^2 - (sum d)^2 / n.
+// The pivot is a mean of n0 of the thread's own n values, so its square
+// distance from their mean is at most S / n0: sum d^2 is at most
+// (1 + n / n0) S, and nothing is lost in the difference, whatever the values.
+template <typename Tin, typename Tout>
+__global__ void __launch_bounds__(32 * kTileWarps, 2) norm_tile_fwd_kernel(const NormParams p, int batches) {
+    using G = Geo<Tin>;
+    extern __shared__ __align__(16) unsigned char units[];
+    __shared__ float2 part[kTileWarps][G::kSteps];
+    __shared__ __align__(8) float stat[2][G::kSteps];  // -mean, 1 / deviation
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, warps = blockDim.x >> 5, sl = lane % G::kLs;
+    const int each = blockDim.x / G::kLs, c0 = t / G::kLs, dim = (int)p.dim;  // channels c0, c0 + each, ...
+    const int64_t tiles = (p.batch * p.L + G::kSteps - 1) / G::kSteps;
+    const uint32_t apart = (uint32_t)(each * p.L * (int)sizeof(Tin)), apart_y = (uint32_t)(each * p.L * (int)sizeof(Tout));
+    const int step = blockDim.x * 16, span = G::kB * step;  // bytes from unit to unit, batch to batch
+    unsigned char *mine = units + t * 16;
+    const int full = dim / each / G::kB;  // batches whose units all threads have
+    const Tin *x = static_cast<const Tin *>(p.x);
+    Tout *y = static_cast<Tout *>(p.y);
+
+    Place at = place_in<Tin>(p, blockIdx.x, sl);
+    for_batches(batches, full, [&](int b, auto whole) {
+        const int c = c0 + b * G::kB * each;
+        copy_batch<Tin, whole.value>(mine + b * span, step, x + at.at + c * p.L, apart, c, each, dim, at.in);
+    });
+    cp_async_commit();
+    // channels of a warp: 8 of every `each` ones
+    const auto channels = [&](int w) {
+        const int k = dim / each, rest = dim - k * each - w * G::kLc;
+        return (float)(k * G::kLc + min(max(rest, 0), G::kLc));
+    };
+    const int have = c0 < dim ? (dim - c0 + each - 1) / each : 0;
+    const float nt = (float)have, inv_n = have ? 1.f / nt : 0.f, inv_w = channels(warp) > 0.f ? 1.f / channels(warp) : 0.f;
+    const float inv_0 = have ? 1.f / (float)min(have, G::kB) : 0.f;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        cp_async_wait_all();
+        float2 np[G::kStats], D[G::kStats], S[G::kStats];  // -pivot, sums of d and d^2
+#pragma unroll
+        for (int k = 0; k < G::kStats; ++k) np[k] = D[k] = S[k] = both(0.f);
+        for_batches(batches, full, [&](int b, auto whole) {
+            Batch<Tin> v;
+            v.read(mine + b * span, step);
+            const int c = c0 + b * G::kB * each;
+            if (b == 0 && !p.rms) {
+#pragma unroll
+                for (int j = 0; j < G::kB; ++j)
+                    if (whole.value || c + j * each < dim) {
+#pragma unroll
+                        for (int k = 0; k < G::kStats; ++k) np[k] = add2(np[k], v.pair(j, k));
+                    }
+#pragma unroll
+                for (int k = 0; k < G::kStats; ++k) np[k] = mul2(np[k], both(-inv_0));
+            }
+#pragma unroll
+            for (int j = 0; j < G::kB; ++j)
+                if (whole.value || c + j * each < dim) {
+#pragma unroll
+                    for (int k = 0; k < G::kStats; ++k) {
+                        const float2 d = add2(v.pair(j, k), np[k]);
+                        D[k] = add2(D[k], d);
+                        S[k] = fma2(d, d, S[k]);
+                    }
+                }
+        });
+        if (!p.rms) {
+            // the thread's mean and squares about it, then the warp's
+            float2 m[G::kStats], mw[G::kStats];
+#pragma unroll
+            for (int k = 0; k < G::kStats; ++k) {
+                const float2 e = mul2(D[k], both(inv_n));
+                S[k] = fma2(neg2(D[k]), e, S[k]);
+                m[k] = add2(e, neg2(np[k]));
+                mw[k] = mul2(m[k], both(nt));
+            }
+            step_sums(mw);
+#pragma unroll
+            for (int k = 0; k < G::kStats; ++k) {
+                D[k] = mul2(mw[k], both(inv_w));
+                const float2 d = add2(m[k], neg2(D[k]));
+                S[k] = fma2(mul2(d, both(nt)), d, S[k]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < G::kStats; ++k) D[k] = both(0.f);
+        }
+        step_sums(S);
+        if (lane < G::kLs) write_steps(part[warp], sl, D, S);
+        __syncthreads();
+        if (t < G::kSteps) {
+            const float2 all = join(&part[0][t], G::kSteps, warps, channels);
+            const float rstd = rsqrtf(fmaf(fmaxf(all.y, 0.f), p.inv_dim, p.eps));
+            stat[0][t] = -all.x, stat[1][t] = rstd;
+            const int64_t s = tile * G::kSteps + t;
+            if (s < p.batch * p.L) {
+                if (p.mean && !p.rms) p.mean[s] = all.x;
+                if (p.rstd) p.rstd[s] = rstd;
+            }
+        }
+        __syncthreads();
+        read_steps(stat[0], sl, np);
+        read_steps(stat[1], sl, S);
+        const Place now = at;
+        const bool more = tile + gridDim.x < tiles;
+        if (more) at = place_in<Tin>(p, tile + gridDim.x, sl);
+        for_batches(batches, full, [&](int b, auto whole) {
+            const int c = c0 + b * G::kB * each;
+            Batch<Tin> v;
+            v.read(mine + b * span, step);
+            Tout *to = y + now.at + c * p.L;
+#pragma unroll
+            for (int j = 0; j < G::kB; ++j) {
+                if (whole.value || c + j * each < dim) {
+                    const float2 w = both(p.weight ? __ldg(p.weight + c + j * each) : 1.f),
+                                 bi = both(p.bias ? __ldg(p.bias + c + j * each) : 0.f);
+                    float2 r[G::kStats];
+#pragma unroll
+                    for (int k = 0; k < G::kStats; ++k) r[k] = fma2(mul2(add2(v.pair(j, k), np[k]), S[k]), w, bi);
+                    if (now.in) store_unit(at_unit(to, apart_y, j), r);
+                }
+            }
+            if (more) copy_batch<Tin, whole.value>(mine + b * span, step, x + at.at + c * p.L, apart, c, each, dim, at.in);
+        });
+        cp_async_commit();
+    }
+}
+
+// Backward: x and dy, and the block's sums of dw and db per channel, in
+// shared memory.
+template <typename T>
+__global__ void __launch_bounds__(32 * kTileWarps, 1) norm_tile_bwd_kernel(const NormParams p, int batches) {
+    using G = Geo<T>;
+    extern __shared__ __align__(16) unsigned char units[];
+    __shared__ float2 part[kTileWarps][G::kSteps];
+    __shared__ __align__(8) float stat[2][G::kSteps];  // sums of v, of v xh
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, warps = blockDim.x >> 5, sl = lane % G::kLs;
+    const int each = blockDim.x / G::kLs, c0 = t / G::kLs, dim = (int)p.dim;
+    const int64_t tiles = (p.batch * p.L + G::kSteps - 1) / G::kSteps;
+    const uint32_t apart = (uint32_t)(each * p.L * (int)sizeof(T));
+    const int step = blockDim.x * 16, span = G::kB * step;
+    unsigned char *mx = units + t * 16, *mg = mx + batches * span;
+    float *acc = reinterpret_cast<float *>(units + 2 * batches * span);  // dw, db
+    const int full = dim / each / G::kB;
+    const T *x = static_cast<const T *>(p.x), *dy = static_cast<const T *>(p.dy);
+    T *dx = static_cast<T *>(p.dx);
+
+    Place at = place_in<T>(p, blockIdx.x, sl);
+    for_batches(batches, full, [&](int b, auto whole) {
+        const int c = c0 + b * G::kB * each;
+        const int64_t from = at.at + c * p.L;
+        if (!whole.value) {  // units of channels that are not there stay zero
+            for (int j = 0; j < G::kB; ++j) {
+                *reinterpret_cast<uint4 *>(mx + b * span + j * step) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4 *>(mg + b * span + j * step) = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+        copy_batch<T, whole.value>(mx + b * span, step, x + from, apart, c, each, dim, at.in);
+        copy_batch<T, whole.value>(mg + b * span, step, dy + from, apart, c, each, dim, at.in);
+    });
+    cp_async_commit();
+    for (int c = t; c < 2 * dim; c += blockDim.x) acc[c] = 0.f;
+    __syncthreads();
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        float2 nm[G::kStats], r[G::kStats], s1[G::kStats], s2[G::kStats];
+#pragma unroll
+        for (int k = 0; k < G::kStats; ++k) {
+            const int64_t s = at.index + 2 * k;
+            nm[k] = p.mean_in ? make_float2(-__ldg(p.mean_in + s), -__ldg(p.mean_in + s + 1)) : both(0.f);
+            r[k] = make_float2(__ldg(p.rstd_in + s), __ldg(p.rstd_in + s + 1));
+            s1[k] = s2[k] = both(0.f);
+        }
+        cp_async_wait_all();
+        for_batches(batches, full, [&](int b, auto whole) {
+            const int c = c0 + b * G::kB * each;
+            Batch<T> vx, vg;
+            vx.read(mx + b * span, step);
+            vg.read(mg + b * span, step);
+            float term[G::kB];
+#pragma unroll
+            for (int j = 0; j < G::kB; ++j) {
+                const int cj = whole.value ? c + j * each : min(c + j * each, dim - 1);
+                const float2 w = both(p.weight ? __ldg(p.weight + cj) : 1.f);
+                float2 sum = both(0.f);
+#pragma unroll
+                for (int k = 0; k < G::kStats; ++k) {
+                    const float2 g = vg.pair(j, k), h = mul2(g, mul2(add2(vx.pair(j, k), nm[k]), r[k]));
+                    s1[k] = fma2(g, w, s1[k]);
+                    s2[k] = fma2(h, w, s2[k]);
+                    sum = add2(sum, h);
+                }
+                term[j] = sum.x + sum.y;
+            }
+            if (p.sums) {
+                const float v = lane_sums<G::kB>(term, lane);
+                const int cs = c + sl * each;  // this lane's unit of the batch
+                if (whole.value || cs < dim) acc[cs] += v;
+            }
+        });
+        step_sums(s1), step_sums(s2);
+        if (lane < G::kLs) write_steps(part[warp], sl, s1, s2);
+        __syncthreads();
+        if (t < G::kSteps) {
+            float2 all = both(0.f);
+            for (int k = 0; k < warps; ++k) all = add2(all, part[k][t]);
+            stat[0][t] = all.x, stat[1][t] = all.y;
+        }
+        __syncthreads();
+        // dx = rstd v - rstd c1 - (x - m) rstd^2 c2, with the step's factors
+        // made once; s1, s2: -rstd c1, -rstd^2 c2
+        read_steps(stat[0], sl, s1);
+        read_steps(stat[1], sl, s2);
+#pragma unroll
+        for (int k = 0; k < G::kStats; ++k) {
+            const float2 f = mul2(r[k], both(-p.inv_dim));
+            s1[k] = p.mean_in ? mul2(s1[k], f) : both(0.f);
+            s2[k] = mul2(mul2(s2[k], f), r[k]);
+        }
+        const Place now = at;
+        const bool more = tile + gridDim.x < tiles;
+        if (more) at = place_in<T>(p, tile + gridDim.x, sl);
+        for_batches(batches, full, [&](int b, auto whole) {
+            const int c = c0 + b * G::kB * each;
+            Batch<T> vx, vg;
+            vx.read(mx + b * span, step);
+            vg.read(mg + b * span, step);
+            T *to = dx + now.at + c * p.L;
+            float term[G::kB];
+#pragma unroll
+            for (int j = 0; j < G::kB; ++j) {
+                const int cj = whole.value ? c + j * each : min(c + j * each, dim - 1);
+                const float2 w = both(p.weight ? __ldg(p.weight + cj) : 1.f);
+                float2 v[G::kStats], sum = both(0.f);
+#pragma unroll
+                for (int k = 0; k < G::kStats; ++k) {
+                    const float2 g = vg.pair(j, k);
+                    sum = add2(sum, g);
+                    v[k] = fma2(add2(vx.pair(j, k), nm[k]), s2[k], fma2(mul2(g, w), r[k], s1[k]));
+                }
+                if (now.in && (whole.value || c + j * each < dim)) store_unit(at_unit(to, apart, j), v);
+                term[j] = sum.x + sum.y;
+            }
+            if (more) {
+                copy_batch<T, whole.value>(mx + b * span, step, x + at.at + c * p.L, apart, c, each, dim, at.in);
+                copy_batch<T, whole.value>(mg + b * span, step, dy + at.at + c * p.L, apart, c, each, dim, at.in);
+            }
+            if (p.sums) {
+                const float v = lane_sums<G::kB>(term, lane);
+                const int cs = c + sl * each;
+                if (whole.value || cs < dim) acc[dim + cs] += v;
+            }
+        });
+        cp_async_commit();
+    }
+    if (p.sums) {
+        __syncthreads();
+        float *out = p.part + (int64_t)blockIdx.x * 2 * p.dim;
+        for (int c = t; c < 2 * dim; c += blockDim.x) out[c] = acc[c];
+    }
+}
+
 // More channels than a cluster's registers hold: passes over the tile, the
 // later ones from the caches.
 template <typename Tin, typename Tout>
@@ -889,21 +1261,32 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const float *part, int6
 // ------------------------------------------------------------------- host
 
 // The launch of a shape: kernel family, threads and blocks.
+enum NormKind { kRows, kRowsWide, kTile, kCluster, kStepsWide };
 struct NormPlan {
-    bool rows, wide;
-    int T, nv, per;    // rows: threads per row, vectors per thread, rows per block
-    int V, steps;      // steps: of a lane's run, of a tile
-    int warps, max_warps, nblk;  // warps per block, blocks per cluster
-    int64_t parts;     // backward: rows of partial sums (blocks or clusters)
+    NormKind kind;
+    bool vec;
+    int T, nv, per;    // rows: threads per row, vectors per thread, rows per block; tile: threads
+    int batches;       // tile: batches of a thread
+    int V, warps, max_warps, nblk;  // cluster: steps of a lane's run, warps per block and at most, blocks
+    int64_t blocks, parts;          // blocks (clusters); rows of partial sums of the backward
 };
 
-constexpr int kRowThreads = 256;  // of a block, unless one row takes more
+constexpr int kRowThreads = 256;          // of a block, unless one row takes more
+constexpr int64_t kSmMost = 228 * 1024;   // shared memory of an SM, and of a block with its reserve of 1 KB
+constexpr int64_t kBlockMost = 227 * 1024;
 
-NormPlan norm_plan(const ss_desc *desc, bool vec) {
+// Dynamic shared memory of the tile kernels.
+int64_t tile_smem(int64_t dim, const NormPlan &pl, bool back) {
+    const int64_t units = (int64_t)pl.batches * pl.T * 64;
+    return back ? 2 * units + 8 * dim : units;
+}
+
+// vec: the innermost axis is whole vectors at every base.
+NormPlan norm_plan(const ss_desc *desc, bool vec, bool back) {
     NormPlan pl{};
     const int64_t sms = layer_sm_count();
-    pl.rows = desc->seqlen == 1;
-    if (pl.rows) {
+    pl.vec = vec;
+    if (desc->seqlen == 1) {
         // The fewest threads that hold a row with three vectors each at most
         // (two where elements are loaded one by one and cost more registers):
         // the backward's sums, parameters and inputs then stay in 128 registers.
@@ -911,36 +1294,62 @@ NormPlan norm_plan(const ss_desc *desc, bool vec) {
         pl.T = 32;
         while (pl.T < 512 && vecs > (int64_t)pl.T * most) pl.T *= 2;
         pl.nv = (int)((vecs + pl.T - 1) / pl.T);
-        pl.wide = pl.nv > most;
-        pl.per = pl.wide || pl.T > kRowThreads ? 1 : kRowThreads / pl.T;
+        pl.kind = pl.nv > most ? kRowsWide : kRows;
+        pl.per = pl.kind == kRowsWide || pl.T > kRowThreads ? 1 : kRowThreads / pl.T;
         const int64_t blocks = (desc->batch + pl.per - 1) / pl.per;
-        const int64_t resident = pl.wide || pl.T > kRowThreads ? sms : 2 * sms;
-        pl.parts = blocks < resident ? blocks : resident;
-    } else {
-        pl.V = !vec ? 1 : desc->in_dtype == SS_BF16 ? 8 : 4;
-        pl.steps = pl.V == 8 ? 64 : 32;
-        // The channels over up to 8 blocks of 8 warps, or of 16.
-        const int64_t need = (desc->dim + kWarpCh - 1) / kWarpCh;
-        pl.max_warps = need <= 64 ? 8 : 16;
-        const int64_t nblk = (need + pl.max_warps - 1) / pl.max_warps;
-        pl.wide = nblk > 8;
-        pl.nblk = pl.wide ? 1 : (int)nblk;
-        pl.warps = pl.wide ? 16 : (int)((need + nblk - 1) / nblk);
-        if (pl.warps < 2) pl.warps = 2;  // a thread for each step of the tile
-        if (pl.wide) pl.steps = 32, pl.V = 1;
-        const int64_t tiles = (desc->batch * desc->seqlen + pl.steps - 1) / pl.steps;
-        const int64_t resident = (sms * (pl.max_warps == 8 ? 2 : 1) + pl.nblk - 1) / pl.nblk;
-        const int64_t rounds = (tiles + resident - 1) / resident;
-        pl.parts = rounds > 0 ? (tiles + rounds - 1) / rounds : 0;
+        const int64_t resident = pl.kind == kRowsWide || pl.T > kRowThreads ? sms : 2 * sms;
+        pl.blocks = pl.parts = blocks < resident ? blocks : resident;
+        return pl;
     }
+    const int64_t n = desc->batch * desc->seqlen;
+    // Tiles of 64 bytes of every channel in shared memory, while they fit:
+    // the channels over T threads, in batches of T.  (8 x 1536 x 2048 bf16:
+    // forward 31 us against 37 in clusters, backward 51 against 69; with rows
+    // that are not whole vectors the same scheme with 4- or 2-byte units took
+    // 69 against 67 and 148 against 137, fp32 of 1000 x 4099 backward 65
+    // against 55: those go to the clusters.)  The backward has dy in x's type;
+    // the bytes between a thread's channels are counted in 32 bits.
+    const int64_t steps = desc->in_dtype == SS_BF16 ? 32 : 16, tiles = (n + steps - 1) / steps;
+    pl.batches = (int)((desc->dim + 511) / 512);
+    pl.T = (int)(((desc->dim + pl.batches - 1) / pl.batches + 31) / 32 * 32);
+    const int64_t smem = tile_smem(desc->dim, pl, back) + 5 * 1024;  // and the kernel's own
+    if (vec && smem <= kBlockMost && !(back && desc->in_dtype != desc->out_dtype) && desc->seqlen <= 1 << 20) {
+        pl.kind = kTile;
+        int64_t resident = 65536 / (pl.T * (back ? 128 : 64));
+        if (resident > kSmMost / (smem + 1024)) resident = kSmMost / (smem + 1024);
+        if (resident < 1) resident = 1;
+        pl.blocks = pl.parts = tiles < resident * sms ? tiles : resident * sms;
+        return pl;
+    }
+    // The channels in the registers of up to 8 blocks of 8 warps, or of 16.
+    const int64_t need = (desc->dim + kWarpCh - 1) / kWarpCh;
+    pl.max_warps = need <= 64 ? 8 : 16;
+    const int64_t nblk = (need + pl.max_warps - 1) / pl.max_warps;
+    if (nblk <= 8) {
+        pl.kind = kCluster;
+        pl.nblk = (int)nblk;
+        pl.warps = (int)((need + nblk - 1) / nblk);
+        if (pl.warps < 2) pl.warps = 2;  // a thread for each step of the tile
+        pl.V = !vec ? 1 : desc->in_dtype == SS_BF16 ? 8 : 4;
+        const int64_t wide = pl.V == 8 ? 64 : 32, count = (n + wide - 1) / wide;
+        const int64_t resident = (sms * (pl.max_warps == 8 ? 2 : 1) + nblk - 1) / nblk;
+        const int64_t rounds = (count + resident - 1) / resident;
+        pl.blocks = count;
+        pl.parts = rounds > 0 ? (count + rounds - 1) / rounds : 0;
+        return pl;
+    }
+    pl.kind = kStepsWide;
+    pl.blocks = (n + 31) / 32;
+    pl.parts = pl.blocks < sms ? pl.blocks : sms;
     return pl;
 }
 
-// Whole vectors: rows of dim elements, or steps of each channel.
-bool norm_vec(const ss_desc *desc, std::initializer_list<const void *> ps) {
+// Whole vectors: rows of dim elements, or steps of each channel.  (The tile
+// kernels read their parameters one by one, the row kernels in vectors.)
+bool norm_vec(const ss_desc *desc, std::initializer_list<const void *> tensors, std::initializer_list<const void *> params) {
     const int64_t inner = desc->seqlen == 1 ? desc->dim : desc->seqlen;
-    const int64_t unit = desc->seqlen == 1 || desc->in_dtype == SS_BF16 ? 8 : 4;
-    return inner % unit == 0 && vec_ok(ps);
+    const int64_t whole = desc->seqlen == 1 || desc->in_dtype == SS_BF16 ? 8 : 4;
+    return inner % whole == 0 && vec_ok(tensors) && (desc->seqlen > 1 || vec_ok(params));
 }
 
 template <typename K>
@@ -979,29 +1388,43 @@ template <typename Tin, typename Tout, int V, int kMaxW>
 cudaError_t launch_steps(bool back, const NormPlan &pl, cudaStream_t s, const NormParams &p) {
     if (back)
         return launch_cluster(norm_steps_bwd_kernel<Tin, Tout, V, kMaxW>, pl.parts * pl.nblk, 32 * pl.warps, pl.nblk, s, p);
-    const int64_t tiles = (p.batch * p.L + pl.steps - 1) / pl.steps;
-    return launch_cluster(norm_steps_fwd_kernel<Tin, Tout, V, kMaxW>, tiles * pl.nblk, 32 * pl.warps, pl.nblk, s, p);
+    return launch_cluster(norm_steps_fwd_kernel<Tin, Tout, V, kMaxW>, pl.blocks * pl.nblk, 32 * pl.warps, pl.nblk, s, p);
 }
 
 template <typename Tin, typename Tout>
-cudaError_t dispatch_norm(bool back, bool vec, const NormPlan &pl, cudaStream_t s, const NormParams &p) {
-    if (pl.wide) {
-        if (pl.rows && back) norm_rows_bwd_wide_kernel<Tin, Tout><<<(unsigned)pl.parts, 1024, 0, s>>>(p);
-        else if (pl.rows) norm_rows_fwd_wide_kernel<Tin, Tout><<<(unsigned)p.batch, 1024, 0, s>>>(p);
-        else if (back) norm_steps_bwd_wide_kernel<Tin, Tout><<<(unsigned)pl.parts, 512, 0, s>>>(p);
-        else norm_steps_fwd_wide_kernel<Tin, Tout><<<(unsigned)((p.batch * p.L + 31) / 32), 512, 0, s>>>(p);
-        return cudaGetLastError();
+cudaError_t launch_tile(bool back, const NormPlan &pl, cudaStream_t s, const NormParams &p) {
+    const auto kernel = back ? norm_tile_bwd_kernel<Tin> : norm_tile_fwd_kernel<Tin, Tout>;
+    const int smem = (int)tile_smem(p.dim, pl, back);
+    if (smem > 40 * 1024) {  // more than the default leaves beside the kernel's own
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
     }
-    if (pl.rows) {
-        if (!vec)
-            return pl.nv == 1 ? launch_rows<Tin, Tout, 1, false>(back, pl, s, p) : launch_rows<Tin, Tout, 2, false>(back, pl, s, p);
-        switch (pl.nv) {
-            case 1: return launch_rows<Tin, Tout, 1, true>(back, pl, s, p);
-            case 2: return launch_rows<Tin, Tout, 2, true>(back, pl, s, p);
-            default: return launch_rows<Tin, Tout, 3, true>(back, pl, s, p);
-        }
-    }
+    kernel<<<(unsigned)pl.blocks, pl.T, smem, s>>>(p, pl.batches);
+    return cudaGetLastError();
+}
+
+template <typename Tin, typename Tout>
+cudaError_t dispatch_norm(bool back, const NormPlan &pl, cudaStream_t s, const NormParams &p) {
     constexpr int kWhole = sizeof(Tin) == 2 ? 8 : 4;
+    switch (pl.kind) {
+        case kRowsWide:
+            if (back) norm_rows_bwd_wide_kernel<Tin, Tout><<<(unsigned)pl.parts, 1024, 0, s>>>(p);
+            else norm_rows_fwd_wide_kernel<Tin, Tout><<<(unsigned)p.batch, 1024, 0, s>>>(p);
+            return cudaGetLastError();
+        case kStepsWide:
+            if (back) norm_steps_bwd_wide_kernel<Tin, Tout><<<(unsigned)pl.parts, 512, 0, s>>>(p);
+            else norm_steps_fwd_wide_kernel<Tin, Tout><<<(unsigned)pl.blocks, 512, 0, s>>>(p);
+            return cudaGetLastError();
+        case kRows:
+            if (!pl.vec)
+                return pl.nv == 1 ? launch_rows<Tin, Tout, 1, false>(back, pl, s, p)
+                                  : launch_rows<Tin, Tout, 2, false>(back, pl, s, p);
+            return pl.nv == 1   ? launch_rows<Tin, Tout, 1, true>(back, pl, s, p)
+                   : pl.nv == 2 ? launch_rows<Tin, Tout, 2, true>(back, pl, s, p)
+                                : launch_rows<Tin, Tout, 3, true>(back, pl, s, p);
+        case kTile: return launch_tile<Tin, Tout>(back, pl, s, p);
+        default: break;
+    }
     if (pl.max_warps == 8)
         return pl.V == 1 ? launch_steps<Tin, Tout, 1, 8>(back, pl, s, p) : launch_steps<Tin, Tout, kWhole, 8>(back, pl, s, p);
     return pl.V == 1 ? launch_steps<Tin, Tout, 1, 16>(back, pl, s, p) : launch_steps<Tin, Tout, kWhole, 16>(back, pl, s, p);
@@ -1044,16 +1467,15 @@ ss_status ss_norm_fwd(const ss_desc *desc, const void *x, const float *weight, c
     NormParams p = norm_params(desc);
     p.x = x, p.weight = weight, p.bias = bias, p.y = y, p.mean = mean, p.rstd = rstd;
     p.eps = eps, p.rms = rms != 0;
-    const bool vec = norm_vec(desc, {x, y, weight, bias});
-    return status_of(SS_LAYER_DISPATCH(desc, dispatch_norm)(false, vec, norm_plan(desc, vec),
-                                                            reinterpret_cast<cudaStream_t>(stream), p));
+    const NormPlan pl = norm_plan(desc, norm_vec(desc, {x, y}, {weight, bias}), false);
+    return status_of(SS_LAYER_DISPATCH(desc, dispatch_norm)(false, pl, reinterpret_cast<cudaStream_t>(stream), p));
 }
 
 size_t ss_norm_bwd_workspace_bytes(const ss_desc *desc) {
     LayerSizes sz;
     if (check_norm(desc, &sz) != SS_OK || sz.elems == 0) return 0;
     // the larger of the two shapes: which one runs depends on the pointers too
-    const int64_t a = norm_plan(desc, false).parts, b = norm_plan(desc, true).parts;
+    const int64_t a = norm_plan(desc, false, true).parts, b = norm_plan(desc, true, true).parts;
     return (size_t)(a > b ? a : b) * 2 * (size_t)desc->dim * sizeof(float);
 }
 
@@ -1084,10 +1506,8 @@ ss_status ss_norm_bwd(const ss_desc *desc, const void *x, const float *weight, c
     }
     p.x = x, p.weight = weight, p.mean_in = mean, p.rstd_in = rstd, p.dy = dy, p.dx = dx;
     p.part = static_cast<float *>(workspace);
-    // dw and db are only written by elements, so weight is the one parameter read in vectors
-    const bool vec = norm_vec(desc, {x, dy, dx, weight, workspace});
-    const NormPlan pl = norm_plan(desc, vec);
-    cudaError_t e = SS_LAYER_DISPATCH(desc, dispatch_norm)(true, vec, pl, s, p);
+    const NormPlan pl = norm_plan(desc, norm_vec(desc, {x, dy, dx}, {weight}), true);  // the workspace is aligned
+    cudaError_t e = SS_LAYER_DISPATCH(desc, dispatch_norm)(true, pl, s, p);
     if (e == cudaSuccess && p.sums) {
         norm_sums_kernel<<<(unsigned)((2 * p.dim + 31) / 32), 1024, 0, s>>>(p.part, pl.parts, p.dim, dweight, dbias);
         e = cudaGetLastError();
