@@ -6,20 +6,27 @@
 // per row (b, d), with the steps before the row taken from a state (or zero)
 // and nothing read across a sequence start.
 //
+// Both directions take 16 steps of a row per thread: two vectors, and their
+// neighbours for the taps (which other threads load too: L1 hits).  Rows are
+// cut in virtual steps (see ss_layer.cuh), so every length uses whole
+// vectors; what lies outside the row is masked after the load.  Steps i and
+// i + 8 of a thread are worked as a pair with the packed arithmetic of two
+// floats: their taps are pairs too, i + j and i + j + 8.
+//
 // Forward: two bytes in and two out per bf16 element against 2 W + 5
-// operations, so it is bound by memory.  The outputs of all rows form one
-// flat array, eight of them per thread, so every length fills the warps and
-// every access is an aligned vector; the W - 1 steps before a thread's own
-// come from the vector before, which its neighbour loads too (an L1 hit).
-// A vector that spans two rows (odd lengths) is worked element by element.
+// operations.
 //
 // Backward: with q_t = dy_t (silu'(p_t)),
 //   dx_s = sum_j w_j q_(s + (W-1) - j),   dw_j = sum_t q_t x_(t - (W-1) + j),   dbias = sum_t q_t.
-// p is recomputed from x.  dw and dbias sum over batch and steps for each
-// channel, so a block (or a cluster of blocks, when the channels are few)
-// takes one channel and all of its batch entries; every thread keeps its W + 1
-// sums in registers over all its vectors and they are joined once at the end,
-// in a fixed order and without a second launch.
+// p is recomputed from x, for the W - 1 steps behind a thread's own as well.
+// dw and dbias sum over batch and steps for each channel, so a block (or a
+// cluster of blocks, when the channels are few) takes one channel and all of
+// its batch entries; every thread keeps its W + 1 sums in registers over all
+// its vectors and they are joined once at the end, in a fixed order and
+// without a second launch.
+//
+// A warp that sees a sequence start in any of its windows takes the path that
+// tests every tap against the starts; the others do not pay for it.
 #pragma once
 
 #include "ss_layer.cuh"
@@ -76,11 +83,109 @@ __device__ __forceinline__ float conv_at(const ConvParams &p, int64_t row, int64
     return acc;
 }
 
+// p (1 / (1 + exp(-p))): exp(-p) may overflow, to a result of zero.
 template <bool kFast>
-__device__ __forceinline__ float silu_of(float v) {
-    float s, c;
-    sigmoid2<kFast>(v, s, c);
-    return v * s;
+__device__ __forceinline__ float2 silu2(float2 v) {
+    if constexpr (kFast) {
+        const float2 t = mul2(v, both(-kLog2e)), u = add2(make_float2(sfu_exp2(t.x), sfu_exp2(t.y)), both(1.f));
+        return mul2(v, make_float2(sfu_rcp(u.x), sfu_rcp(u.y)));
+    } else {
+        return make_float2(v.x / (1.f + expf(-v.x)), v.y / (1.f + expf(-v.y)));
+    }
+}
+
+// dy silu'(p) = dy s (1 + p (1 - s)).
+template <bool kFast>
+__device__ __forceinline__ float2 conv_slope(float2 pre, float2 dy) {
+    float2 s;
+    if constexpr (kFast) {
+        const float2 t = mul2(pre, both(-kLog2e)), u = add2(make_float2(sfu_exp2(t.x), sfu_exp2(t.y)), both(1.f));
+        s = make_float2(sfu_rcp(u.x), sfu_rcp(u.y));
+    } else {
+        s = make_float2(1.f / (1.f + expf(-pre.x)), 1.f / (1.f + expf(-pre.y)));
+    }
+    return mul2(dy, mul2(s, fma2(pre, add2(both(1.f), neg2(s)), both(1.f))));
+}
+
+constexpr int kSpan = 16;  // steps of a thread
+
+// Where a thread's steps lie: step t0 of the row, element e.
+struct Span {
+    int64_t t0, e;
+    int lo, hi;  // its steps lo .. hi-1 are in the row
+};
+__device__ __forceinline__ Span span_of(int64_t e0, int64_t v, int64_t L) {
+    Span s;
+    s.t0 = v * kSpan - (e0 & (kV - 1));
+    s.e = e0 + s.t0;
+    s.lo = s.t0 < 0 ? (int)-s.t0 : 0;
+    s.hi = L - s.t0 < kSpan ? (int)(L - s.t0) : kSpan;
+    return s;
+}
+__device__ __forceinline__ int64_t spans_of(int64_t L) { return (L + kV - 1 + kSpan - 1) / kSpan; }
+
+// The vector at element e (which need not lie in the tensor of n elements).
+template <typename T>
+__device__ __forceinline__ void load_at(Vec8<T> &r, const T *p, int64_t e, int64_t n, bool vec) {
+    load8(r, p, e, clamp8(-e), clamp8(n - e), vec);
+}
+
+// x at steps t0 - (W-1) .. of a thread, kN vectors of its own and behind:
+// pairs (k, k + 8).  Outside the row: the state before it, zero behind.
+template <typename T, int W, int kVecs>
+struct Window {
+    static constexpr int kN = W - 1 + kV * (kVecs - 1) + (kVecs == 2 ? kV : W - 1);  // values
+    static constexpr int kPairs = kN - kV;
+    float2 v[kPairs];
+    // value k is v[k].x (k < kPairs) and v[k - 8].y (k >= 8)
+    __device__ __forceinline__ void set(int k, float f) {
+        if (k < kPairs) v[k].x = f;
+        if (k >= kV) v[k - kV].y = f;
+    }
+    __device__ __forceinline__ float get(int k) const { return k < kPairs ? v[k].x : v[k - kV].y; }
+    __device__ __forceinline__ void load(const ConvParams &p, const T *x, const Span &s, int64_t row, int64_t n) {
+        Vec8<T> q[kVecs + 1];
+#pragma unroll
+        for (int i = 0; i <= kVecs; ++i) load_at(q[i], x, s.e + (i - 1) * kV, n, p.vec);
+#pragma unroll
+        for (int k = 0; k < kN; ++k) set(k, q[(k + kV - (W - 1)) / kV][(k + kV - (W - 1)) % kV]);
+        if (s.t0 < W - 1 || s.t0 + kN - (W - 1) > p.L) {  // the row's ends
+#pragma unroll
+            for (int k = 0; k < kN; ++k) {
+                const int64_t t = s.t0 - (W - 1) + k;
+                if (t < 0 || t >= p.L) set(k, 0.f);
+            }
+            if (p.h0 && s.t0 < W - 1) {
+#pragma unroll
+                for (int k = 0; k < 2 * (W - 1) + kV - 1 && k < kN; ++k) {  // t0 >= -7: steps -(W-1) .. -1 lie here
+                    const int64_t t = s.t0 - (W - 1) + k;
+                    if (t < 0 && t >= -(W - 1)) set(k, load_elem(static_cast<const T *>(p.h0), row * (W - 1) + (W - 1) + t));
+                }
+            }
+        }
+    }
+};
+
+// Bit k: a sequence starts at step t0 - (W-1) + k, for kBits steps.
+template <int W, int kBits>
+__device__ __forceinline__ uint32_t window_starts(const ConvParams &p, int64_t b, int64_t t0) {
+    uint32_t m = 0;
+    const int64_t first = t0 - (W - 1);
+#pragma unroll
+    for (int k = 0; k < kBits; k += kV) {
+        const int64_t t = first + k;
+        m |= start_bits(p.reset, b * p.L + t, p.batch * p.L, clamp8(-t), clamp8(p.L - t)) << k;
+    }
+    return kBits < 32 ? m & ((1u << kBits) - 1u) : m;
+}
+
+// cut[j], bit k: a start lies between tap j of output k and the output's own
+// step (window positions k + j + 1 .. k + W - 1).
+template <int W>
+__device__ __forceinline__ void cuts_of(uint32_t m, uint32_t (&cut)[W]) {
+    cut[W - 1] = 0;
+#pragma unroll
+    for (int j = W - 2; j >= 0; --j) cut[j] = cut[j + 1] | m >> (j + 1);
 }
 
 template <typename Tin, typename Tout, int W, bool kR>
@@ -97,98 +202,61 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(const ConvParams p) {
         put(static_cast<Tin *>(p.last), i, seen ? conv_input<Tin, W>(p, row, t) : 0.f);
         return;
     }
-    const int64_t e = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * kV;
-    if (e >= n) return;
-    const int64_t row = n <= INT_MAX ? (int64_t)((uint32_t)e / (uint32_t)L) : e / L;
-    const int64_t t0 = e - row * L;
-    const int64_t b = rows <= INT_MAX ? (int64_t)((uint32_t)row / (uint32_t)p.dim) : row / p.dim;
-    const int64_t d = row - b * p.dim;
-    const Tin *x = static_cast<const Tin *>(p.x);
-    Tout *y = static_cast<Tout *>(p.y);
-    float out[kV];
-    if (t0 + kV <= L) {
-        float w[W];
+    const int64_t q = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, nv = spans_of(L);
+    const bool there = q < rows * nv;  // (the threads behind stay for their warp's vote)
+    const int64_t row = !there ? 0 : rows * nv <= INT_MAX ? (int64_t)((uint32_t)q / (uint32_t)nv) : q / nv;
+    const int64_t b = (int64_t)((uint32_t)row / (uint32_t)p.dim), d = row - b * p.dim;
+    Span s = span_of(row * L, there ? q - row * nv : 0, L);
+    if (!there) s.hi = 0;
+    float w[W];
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[j] = __ldg(p.weight + d * W + j);
-        const float bias = p.bias ? __ldg(p.bias + d) : 0.f;
-        float win[W - 1 + kV];  // steps t0 - (W-1) .. t0 + 7
-        Vec8<Tin> own;
-        load8(own, x, e, 0, kV, p.vec);
-        if (t0 >= W - 1) {
-            Vec8<Tin> prev;
-            if (p.vec) prev.load(x, e - kV);
-            else prev.load_part(x, e - kV, kV - (W - 1), kV);
+    for (int j = 0; j < W; ++j) w[j] = __ldg(p.weight + d * W + j);
+    const float bias = p.bias ? __ldg(p.bias + d) : 0.f;
+    Window<Tin, W, 2> x;
+    x.load(p, static_cast<const Tin *>(p.x), s, row, n);
+    float2 out[kV];
+    uint32_t m = 0;
+    if constexpr (kR) m = window_starts<W, W - 1 + kSpan>(p, b, s.t0);
+    if (kR && __any_sync(0xffffffffu, m != 0)) {
+        uint32_t cut[W];
+        cuts_of<W>(m, cut);
 #pragma unroll
-            for (int k = 0; k < W - 1; ++k) win[k] = prev[kV - (W - 1) + k];
-        } else {
+        for (int i = 0; i < kV; ++i) {
+            out[i] = both(bias);
 #pragma unroll
-            for (int k = 0; k < W - 1; ++k) win[k] = conv_input<Tin, W>(p, row, t0 - (W - 1) + k);
-        }
-#pragma unroll
-        for (int i = 0; i < kV; ++i) win[W - 1 + i] = own[i];
-        if constexpr (kR) {
-            // bit k: a sequence starts at step t0 - (W-1) + k
-            const int lo = t0 >= kV ? 0 : (int)(kV - t0);
-            const uint32_t before = start_bits(p.reset, b * L + t0 - kV, p.batch * L, lo, kV) >> (kV - (W - 1));
-            const uint32_t m = before | start_bits(p.reset, b * L + t0, p.batch * L, 0, kV) << (W - 1);
-#pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                float acc = bias;
-                bool seen = true;
-                float xs[W];
-#pragma unroll
-                for (int j = W - 1; j >= 0; --j) {
-                    xs[j] = seen ? win[i + j] : 0.f;
-                    seen = seen && !(m >> (i + j) & 1u);
-                }
-#pragma unroll
-                for (int j = 0; j < W; ++j) acc = fmaf(w[j], xs[j], acc);
-                out[i] = acc;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                float acc = bias;
-#pragma unroll
-                for (int j = 0; j < W; ++j) acc = fmaf(w[j], win[i + j], acc);
-                out[i] = acc;
+            for (int j = 0; j < W; ++j) {
+                float2 v = x.v[i + j];
+                if (cut[j] >> i & 1u) v.x = 0.f;
+                if (cut[j] >> (i + kV) & 1u) v.y = 0.f;
+                out[i] = fma2(both(w[j]), v, out[i]);
             }
         }
     } else {
-#pragma unroll 1
-        for (int i = 0; i < kV; ++i) {
-            if (e + i >= n) break;
-            const int64_t r = (e + i) / L, c = r % p.dim;
-            float w[W];
 #pragma unroll
-            for (int j = 0; j < W; ++j) w[j] = __ldg(p.weight + c * W + j);
-            const float v = conv_at<Tin, W>(p, r, e + i - r * L, w, p.bias ? __ldg(p.bias + c) : 0.f);
-            put(y, e + i, p.silu ? silu_of<kFast>(v) : v);
+        for (int i = 0; i < kV; ++i) {
+            out[i] = both(bias);
+#pragma unroll
+            for (int j = 0; j < W; ++j) out[i] = fma2(both(w[j]), x.v[i + j], out[i]);
         }
-        return;
     }
     if (p.silu) {
 #pragma unroll
-        for (int i = 0; i < kV; ++i) out[i] = silu_of<kFast>(out[i]);
+        for (int i = 0; i < kV; ++i) out[i] = silu2<kFast>(out[i]);
     }
-    store8(y, e, 0, kV, p.vec, out);
-}
-
-// q_t from p_t and dy_t.
-template <bool kFast>
-__device__ __forceinline__ float conv_slope(float pre, float dy, bool silu) {
-    if (!silu) return dy;
-    float s, c;
-    sigmoid2<kFast>(pre, s, c);
-    return dy * (s * fmaf(pre, c, 1.f));
+    float y0[kV], y1[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) y0[i] = out[i].x, y1[i] = out[i].y;
+    Tout *y = static_cast<Tout *>(p.y);
+    store8(y, s.e, s.lo, s.hi, p.vec, y0);
+    store8(y, s.e + kV, s.lo - kV, s.hi - kV, p.vec, y1);
 }
 
 constexpr int kConvBwdThreads = 256;
 
 template <typename Tin, typename Tout, int W, bool kR>
-__global__ void __launch_bounds__(kConvBwdThreads) conv_bwd_kernel(const ConvParams p, int nblk) {
+__global__ void __launch_bounds__(kConvBwdThreads, 2) conv_bwd_kernel(const ConvParams p, int nblk) {
     constexpr bool kFast = sizeof(Tin) == 2;
-    const int64_t L = p.L;
+    const int64_t L = p.L, n = p.batch * p.dim * L;
     const int64_t d = blockIdx.x / nblk;  // the blocks of a channel follow one another: one cluster
     const int rank = (int)(blockIdx.x % nblk);
     const Tin *x = static_cast<const Tin *>(p.x);
@@ -200,109 +268,116 @@ __global__ void __launch_bounds__(kConvBwdThreads) conv_bwd_kernel(const ConvPar
     for (int j = 0; j < W; ++j) w[j] = __ldg(p.weight + d * W + j);
     const float bias = p.bias ? __ldg(p.bias + d) : 0.f;
 
-    float sum[W + 1];  // dw_j, dbias
+    float2 sum2[W + 1];  // dw_j, dbias, of the two halves of the thread's steps
 #pragma unroll
-    for (int j = 0; j <= W; ++j) sum[j] = 0.f;
+    for (int j = 0; j <= W; ++j) sum2[j] = both(0.f);
 
-    // Vectors of the channel's rows, in virtual steps: nv for each batch entry.
-    const int64_t nv = (L + 2 * kV - 2) / kV;
-    const int64_t total = p.batch * nv, stride = (int64_t)nblk * blockDim.x;
-    for (int64_t q = (int64_t)rank * blockDim.x + threadIdx.x; q < total; q += stride) {
-        const int64_t b = q / nv;
-        const int64_t row = b * p.dim + d, e0 = row * L;
-        const int64_t t0 = (q - b * nv) * kV - (e0 & (kV - 1)), e = e0 + t0;
-        const int lo = clamp8(-t0), hi = clamp8(L - t0);
-        if (hi <= lo) continue;
-        constexpr int kWin = kV + 2 * (W - 1);  // x at steps t0 - (W-1) .. t0 + 7 + (W-1)
-        constexpr int kOut = kV + W - 1;        // q at steps t0 .. t0 + 7 + (W-1)
-        float win[kWin], slope[kOut];
+    const int64_t nv = spans_of(L), total = p.batch * nv, stride = (int64_t)nblk * blockDim.x;
+    for (int64_t q0 = (int64_t)rank * blockDim.x; q0 < total; q0 += stride) {
+        const int64_t q = q0 + threadIdx.x;
+        const bool there = q < total;
+        const int64_t b = !there ? 0 : total <= INT_MAX ? (int64_t)((uint32_t)q / (uint32_t)nv) : q / nv;
+        const int64_t row = b * p.dim + d;
+        Span s = span_of(row * L, there ? q - b * nv : 0, L);
+        constexpr int kOut = kV + W - 1;  // pairs of outputs: the thread's steps and W - 1 behind
+        Window<Tin, W, 3> win;
+        win.load(p, x, s, row, n);
+        float2 slope[kOut];  // first dy: outputs k and k + 8
         {
-            Vec8<Tin> v;
-            const bool in = vec && t0 >= kV && t0 + 2 * kV <= L;  // all three vectors lie in the row
-            if (in) {
-                v.load(x, e - kV);
+            Vec8<Tout> u[3];
 #pragma unroll
-                for (int k = 0; k < W - 1; ++k) win[k] = v[kV - (W - 1) + k];
-                v.load(x, e);
+            for (int i = 0; i < 3; ++i) load_at(u[i], dy, s.e + i * kV, n, vec);
 #pragma unroll
-                for (int k = 0; k < kV; ++k) win[W - 1 + k] = v[k];
-                v.load(x, e + kV);
-#pragma unroll
-                for (int k = 0; k < W - 1; ++k) win[W - 1 + kV + k] = v[k];
-                Vec8<Tout> u;
-                u.load(dy, e);
-#pragma unroll
-                for (int k = 0; k < kV; ++k) slope[k] = u[k];
-                u.load(dy, e + kV);
-#pragma unroll
-                for (int k = 0; k < W - 1; ++k) slope[kV + k] = u[k];
-            } else {
-#pragma unroll
-                for (int k = 0; k < kWin; ++k) {
-                    const int64_t t = t0 - (W - 1) + k;
-                    win[k] = t >= -(W - 1) && t < L ? conv_input<Tin, W>(p, row, t) : 0.f;
-                }
+            for (int k = 0; k < kOut; ++k) slope[k] = make_float2(u[k / kV][k % kV], u[k / kV + 1][k % kV]);
+            if (!there || s.t0 < 0 || s.t0 + kSpan + W - 1 > L) {
+                const int64_t hi = there ? L - s.t0 : 0;
 #pragma unroll
                 for (int k = 0; k < kOut; ++k) {
-                    const int64_t t = t0 + k;
-                    slope[k] = t >= 0 && t < L ? load_elem(dy, e0 + t) : 0.f;
+                    if (k < s.lo || k >= hi) slope[k].x = 0.f;
+                    if (k + kV < s.lo || k + kV >= hi) slope[k].y = 0.f;
                 }
             }
+            if (!there) s.hi = 0;
         }
-        uint32_t m = 0;  // bit k: a sequence starts at step t0 - (W-1) + k
-        if constexpr (kR) {
-#pragma unroll
-            for (int k = 0; k < kWin; ++k) {
-                const int64_t t = t0 - (W - 1) + k;
-                if (t >= 0 && t < L && starts_at(p, b, t)) m |= 1u << k;
-            }
-        }
-        // p_t and q_t; a tap j of output k reads win[k + j] unless a start lies behind it
-        const auto cut = [&](int k, int j) {  // a start in the steps after win[k + j] up to output k's own
-            return kR && (m >> (k + j + 1) & ((1u << (W - 1 - j)) - 1u)) != 0;
+        uint32_t m = 0;
+        if constexpr (kR) m = window_starts<W, 2 * (W - 1) + kSpan>(p, b, s.t0);
+        const bool cutting = kR && __any_sync(0xffffffffu, m != 0);
+        uint32_t cut[W];
+        cuts_of<W>(m, cut);
+        const auto tap = [&](float2 v, int j, int k) {  // v, of tap j of outputs k, k + 8, or zero behind a start
+            if (kR && (cut[j] >> k & 1u)) v.x = 0.f;
+            if (kR && (cut[j] >> (k + kV) & 1u)) v.y = 0.f;
+            return v;
         };
+        if (silu) {
+            if (cutting) {
 #pragma unroll
-        for (int k = 0; k < kOut; ++k) {
-            if (silu) {
-                float pre = bias;
+                for (int k = 0; k < kOut; ++k) {
+                    float2 pre = both(bias);
 #pragma unroll
-                for (int j = 0; j < W; ++j) pre = fmaf(w[j], cut(k, j) ? 0.f : win[k + j], pre);
-                const bool inside = t0 + k >= 0 && t0 + k < L;
-                slope[k] = inside ? conv_slope<kFast>(pre, slope[k], true) : 0.f;
-            }
-        }
-        float g[kV];
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            float acc = 0.f;
-#pragma unroll
-            for (int j = 0; j < W; ++j) {  // output step i + j, whose tap W-1-j reads step i
-                const int k = i + j;
-                acc = cut(k, W - 1 - j) ? acc : fmaf(w[W - 1 - j], slope[k], acc);
-            }
-            g[i] = acc;
-        }
-        if (p.dlast && t0 + kV > L - (W - 1)) {
-            bool seen = true;
-            for (int64_t s = L - 1; s >= t0 && s >= 0 && s >= L - (W - 1); --s) {
-                const int64_t i = s - t0;
-                if (i < kV && seen) {
-#pragma unroll
-                    for (int k = 0; k < kV; ++k)
-                        if (k == i) g[k] += load_elem(static_cast<const Tin *>(p.dlast), row * (W - 1) + s - (L - (W - 1)));
+                    for (int j = 0; j < W; ++j) pre = fma2(both(w[j]), tap(win.v[k + j], j, k), pre);
+                    slope[k] = conv_slope<kFast>(pre, slope[k]);
                 }
-                if (starts_at(p, b, s)) seen = false;
+            } else {
+#pragma unroll
+                for (int k = 0; k < kOut; ++k) {
+                    float2 pre = both(bias);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) pre = fma2(both(w[j]), win.v[k + j], pre);
+                    slope[k] = conv_slope<kFast>(pre, slope[k]);
+                }
             }
         }
-        store8(dx, e, lo, hi, vec, g);
-        // the channel's sums, over this vector's own outputs
+        float2 g[kV];
+        // output i + j reads step i with its tap W-1-j; the sums take the thread's own outputs
+        if (cutting) {
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
+            for (int i = 0; i < kV; ++i) {
+                g[i] = both(0.f);
 #pragma unroll
-            for (int j = 0; j < W; ++j) sum[j] = cut(i, j) ? sum[j] : fmaf(slope[i], win[i + j], sum[j]);
-            sum[W] += slope[i];
+                for (int j = 0; j < W; ++j) {
+                    g[i] = fma2(both(w[W - 1 - j]), tap(slope[i + j], W - 1 - j, i + j), g[i]);
+                    const float2 xv = tap(win.v[i + j], j, i);
+                    sum2[j] = fma2(slope[i], xv, sum2[j]);
+                }
+                sum2[W] = add2(sum2[W], slope[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                g[i] = both(0.f);
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    g[i] = fma2(both(w[W - 1 - j]), slope[i + j], g[i]);
+                    sum2[j] = fma2(slope[i], win.v[i + j], sum2[j]);
+                }
+                sum2[W] = add2(sum2[W], slope[i]);
+            }
         }
+        if (p.dlast && there && s.t0 + kSpan > L - (W - 1)) {  // the last state's elements are inputs too
+            bool seen = true;
+            for (int64_t t = L - 1; t >= s.t0 && t >= 0 && t >= L - (W - 1); --t) {
+                const int i = (int)(t - s.t0);
+                if (i < kSpan && seen) {
+                    const float f = load_elem(static_cast<const Tin *>(p.dlast), row * (W - 1) + t - (L - (W - 1)));
+#pragma unroll
+                    for (int k = 0; k < kV; ++k) {
+                        if (k == i) g[k].x += f;
+                        if (k + kV == i) g[k].y += f;
+                    }
+                }
+                if (starts_at(p, b, t)) seen = false;
+            }
+        }
+        float g0[kV], g1[kV];
+#pragma unroll
+        for (int i = 0; i < kV; ++i) g0[i] = g[i].x, g1[i] = g[i].y;
+        store8(dx, s.e, s.lo, s.hi, vec, g0);
+        store8(dx, s.e + kV, s.lo - kV, s.hi - kV, vec, g1);
     }
+    float sum[W + 1];
+#pragma unroll
+    for (int j = 0; j <= W; ++j) sum[j] = sum2[j].x + sum2[j].y;
 
     // the state's gradient: outputs 0 .. W-2 reach it
     if (p.dh0) {
@@ -315,7 +390,8 @@ __global__ void __launch_bounds__(kConvBwdThreads) conv_bwd_kernel(const ConvPar
                 if (starts_at(p, b, t)) seen = false;
                 if (!seen) break;
                 const float pre = silu ? conv_at<Tin, W>(p, row, t, w, bias) : 0.f;
-                const float slope = conv_slope<kFast>(pre, load_elem(dy, row * L + t), silu);
+                const float dyt = load_elem(dy, row * L + t);
+                const float slope = silu ? conv_slope<kFast>(both(pre), both(dyt)).x : dyt;
 #pragma unroll
                 for (int j = 0; j < W; ++j)
                     if (j == k - t) acc = fmaf(w[j], slope, acc);

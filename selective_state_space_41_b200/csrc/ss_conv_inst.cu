@@ -17,8 +17,8 @@ using Tout = SS_INST_TOUT;
 
 template <int W>
 cudaError_t fwd(cudaStream_t s, ConvParams &p) {
-    const int64_t n = p.batch * p.dim * p.L;
-    p.main_blocks = (n + kV * 256 - 1) / (kV * 256);
+    const int64_t spans = p.batch * p.dim * ((p.L + kV - 1 + kSpan - 1) / kSpan);
+    p.main_blocks = (spans + 255) / 256;
     const int64_t tail = p.last ? (p.batch * p.dim * (W - 1) + 255) / 256 : 0;
     if (p.main_blocks + tail > INT_MAX) return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)(p.main_blocks + tail);
@@ -31,7 +31,7 @@ template <int W>
 cudaError_t bwd(cudaStream_t s, const ConvParams &p) {
     // Blocks per channel: enough for about eight blocks per SM, no more than
     // the channel's vectors feed.
-    const int64_t vecs = p.batch * ((p.L + 2 * kV - 2) / kV);
+    const int64_t vecs = p.batch * ((p.L + kV - 1 + kSpan - 1) / kSpan);
     int nblk = 1;
     while (nblk < 8 && p.dim * nblk < (int64_t)layer_sm_count() * 8 && vecs > (int64_t)nblk * kConvBwdThreads) nblk *= 2;
     cudaLaunchConfig_t cfg{};

@@ -111,7 +111,7 @@ template <typename T>
 __device__ __forceinline__ void store8(T *p, int64_t e, int lo, int hi, bool vec, const float (&v)[kV]) {
     if (vec && lo <= 0 && hi >= kV) {
         store_vec(p + e, v);
-    } else {
+    } else if (hi > lo) {
 #pragma unroll
         for (int i = 0; i < kV; ++i)
             if (i >= lo && i < hi) put(p, e + i, v[i]);
