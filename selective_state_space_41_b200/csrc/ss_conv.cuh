@@ -45,14 +45,16 @@ struct ConvParams {
     int silu, vec;
     int width;            // decoding step
     int64_t main_blocks;  // forward: blocks of the outputs; the rest write the last state
+    Divisor by_spans, by_dim;  // spans of a row, channels
+    int small;            // the spans count in 31 bits (forward: of all rows; backward: of a channel)
 };
 
 cudaError_t conv_fwd_f32_f32(int width, cudaStream_t s, ConvParams &p);
 cudaError_t conv_fwd_bf16_bf16(int width, cudaStream_t s, ConvParams &p);
 cudaError_t conv_fwd_bf16_f32(int width, cudaStream_t s, ConvParams &p);
-cudaError_t conv_bwd_f32_f32(int width, cudaStream_t s, const ConvParams &p);
-cudaError_t conv_bwd_bf16_bf16(int width, cudaStream_t s, const ConvParams &p);
-cudaError_t conv_bwd_bf16_f32(int width, cudaStream_t s, const ConvParams &p);
+cudaError_t conv_bwd_f32_f32(int width, cudaStream_t s, ConvParams &p);
+cudaError_t conv_bwd_bf16_bf16(int width, cudaStream_t s, ConvParams &p);
+cudaError_t conv_bwd_bf16_f32(int width, cudaStream_t s, ConvParams &p);
 
 // x at step t of a row (t < 0: the state), in 32 bits.
 template <typename T, int W>
@@ -109,25 +111,27 @@ __device__ __forceinline__ float2 conv_slope(float2 pre, float2 dy) {
 
 constexpr int kSpan = 16;  // steps of a thread
 
-// Where a thread's steps lie: step t0 of the row, element e.
+// Where a thread's steps lie: step t0 of the row, element e; head and tail
+// are the steps from the row's start and to its end, counted up to 64.
 struct Span {
     int64_t t0, e;
-    int lo, hi;  // its steps lo .. hi-1 are in the row
+    int head, tail;
+    __device__ __forceinline__ int lo(int i) const { return min(max(-(head + i), 0), kV); }  // of the vector at t0 + i
+    __device__ __forceinline__ int hi(int i) const { return min(max(tail - i, 0), kV); }
 };
 __device__ __forceinline__ Span span_of(int64_t e0, int64_t v, int64_t L) {
     Span s;
     s.t0 = v * kSpan - (e0 & (kV - 1));
     s.e = e0 + s.t0;
-    s.lo = s.t0 < 0 ? (int)-s.t0 : 0;
-    s.hi = L - s.t0 < kSpan ? (int)(L - s.t0) : kSpan;
+    s.head = (int)min(s.t0, (int64_t)64);
+    s.tail = (int)min(L - s.t0, (int64_t)64);  // -6 at the least
     return s;
 }
-__device__ __forceinline__ int64_t spans_of(int64_t L) { return (L + kV - 1 + kSpan - 1) / kSpan; }
-
-// The vector at element e (which need not lie in the tensor of n elements).
-template <typename T>
-__device__ __forceinline__ void load_at(Vec8<T> &r, const T *p, int64_t e, int64_t n, bool vec) {
-    load8(r, p, e, clamp8(-e), clamp8(n - e), vec);
+// Spans of a row: the largest shift of a row's start is 8 less the largest
+// power of two in L (8 at most).
+__host__ __device__ __forceinline__ int64_t spans_of(int64_t L) {
+    const int64_t two = L % 8 == 0 ? 8 : L % 4 == 0 ? 4 : L % 2 == 0 ? 2 : 1;
+    return (L + kV - two + kSpan - 1) / kSpan;
 }
 
 // x at steps t0 - (W-1) .. of a thread, kN vectors of its own and behind:
@@ -143,24 +147,24 @@ struct Window {
         if (k >= kV) v[k - kV].y = f;
     }
     __device__ __forceinline__ float get(int k) const { return k < kPairs ? v[k].x : v[k - kV].y; }
-    __device__ __forceinline__ void load(const ConvParams &p, const T *x, const Span &s, int64_t row, int64_t n) {
+    // inner: all of its vectors lie in the row and are whole
+    __device__ __forceinline__ void load(const ConvParams &p, const T *x, const Span &s, int64_t row, int64_t n, bool inner) {
         Vec8<T> q[kVecs + 1];
+        if (inner) {
 #pragma unroll
-        for (int i = 0; i <= kVecs; ++i) load_at(q[i], x, s.e + (i - 1) * kV, n, p.vec);
+            for (int i = 0; i <= kVecs; ++i) q[i].load(x + s.e, (i - 1) * kV);
+        } else {
+#pragma unroll
+            for (int i = 0; i <= kVecs; ++i)
+                load_row8(q[i], x, s.e + (i - 1) * kV, n, s.lo((i - 1) * kV), s.hi((i - 1) * kV), p.vec);
+        }
 #pragma unroll
         for (int k = 0; k < kN; ++k) set(k, q[(k + kV - (W - 1)) / kV][(k + kV - (W - 1)) % kV]);
-        if (s.t0 < W - 1 || s.t0 + kN - (W - 1) > p.L) {  // the row's ends
+        if (p.h0 && s.head < W - 1) {
 #pragma unroll
-            for (int k = 0; k < kN; ++k) {
-                const int64_t t = s.t0 - (W - 1) + k;
-                if (t < 0 || t >= p.L) set(k, 0.f);
-            }
-            if (p.h0 && s.t0 < W - 1) {
-#pragma unroll
-                for (int k = 0; k < 2 * (W - 1) + kV - 1 && k < kN; ++k) {  // t0 >= -7: steps -(W-1) .. -1 lie here
-                    const int64_t t = s.t0 - (W - 1) + k;
-                    if (t < 0 && t >= -(W - 1)) set(k, load_elem(static_cast<const T *>(p.h0), row * (W - 1) + (W - 1) + t));
-                }
+            for (int k = 0; k < 2 * (W - 1) + kV - 1 && k < kN; ++k) {  // head >= -7: steps -(W-1) .. -1 lie here
+                const int t = s.head - (W - 1) + k;
+                if (t < 0 && t >= -(W - 1)) set(k, load_elem(static_cast<const T *>(p.h0), row * (W - 1) + (W - 1) + t));
             }
         }
     }
@@ -204,16 +208,17 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(const ConvParams p) {
     }
     const int64_t q = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, nv = spans_of(L);
     const bool there = q < rows * nv;  // (the threads behind stay for their warp's vote)
-    const int64_t row = !there ? 0 : rows * nv <= INT_MAX ? (int64_t)((uint32_t)q / (uint32_t)nv) : q / nv;
-    const int64_t b = (int64_t)((uint32_t)row / (uint32_t)p.dim), d = row - b * p.dim;
+    const uint32_t row = !there ? 0u : p.small ? divide((uint32_t)q, p.by_spans) : (uint32_t)(q / nv);
+    const uint32_t b = divide(row, p.by_dim), d = row - b * p.by_dim.d;
     Span s = span_of(row * L, there ? q - row * nv : 0, L);
-    if (!there) s.hi = 0;
+    if (!there) s.tail = -kSpan;
+    const bool whole = p.vec && s.head >= 0 && s.tail >= kSpan, inner = whole && s.head >= kV;
     float w[W];
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j] = __ldg(p.weight + d * W + j);
+    for (int j = 0; j < W; ++j) w[j] = __ldg(p.weight + (int64_t)d * W + j);
     const float bias = p.bias ? __ldg(p.bias + d) : 0.f;
     Window<Tin, W, 2> x;
-    x.load(p, static_cast<const Tin *>(p.x), s, row, n);
+    x.load(p, static_cast<const Tin *>(p.x), s, row, n, inner);
     float2 out[kV];
     uint32_t m = 0;
     if constexpr (kR) m = window_starts<W, W - 1 + kSpan>(p, b, s.t0);
@@ -246,9 +251,14 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(const ConvParams p) {
     float y0[kV], y1[kV];
 #pragma unroll
     for (int i = 0; i < kV; ++i) y0[i] = out[i].x, y1[i] = out[i].y;
-    Tout *y = static_cast<Tout *>(p.y);
-    store8(y, s.e, s.lo, s.hi, p.vec, y0);
-    store8(y, s.e + kV, s.lo - kV, s.hi - kV, p.vec, y1);
+    Tout *y = static_cast<Tout *>(p.y) + s.e;
+    if (whole) {
+        store_vec(y, y0);
+        store_vec(y + kV, y1);
+    } else {
+        store8(y, 0, s.lo(0), s.hi(0), p.vec, y0);
+        store8(y, kV, s.lo(kV), s.hi(kV), p.vec, y1);
+    }
 }
 
 constexpr int kConvBwdThreads = 256;
@@ -276,28 +286,27 @@ __global__ void __launch_bounds__(kConvBwdThreads, 2) conv_bwd_kernel(const Conv
     for (int64_t q0 = (int64_t)rank * blockDim.x; q0 < total; q0 += stride) {
         const int64_t q = q0 + threadIdx.x;
         const bool there = q < total;
-        const int64_t b = !there ? 0 : total <= INT_MAX ? (int64_t)((uint32_t)q / (uint32_t)nv) : q / nv;
+        const int64_t b = !there ? 0 : p.small ? (int64_t)divide((uint32_t)q, p.by_spans) : q / nv;
         const int64_t row = b * p.dim + d;
         Span s = span_of(row * L, there ? q - b * nv : 0, L);
         constexpr int kOut = kV + W - 1;  // pairs of outputs: the thread's steps and W - 1 behind
         Window<Tin, W, 3> win;
-        win.load(p, x, s, row, n);
+        if (!there) s.tail = -kSpan;
+        const bool whole = vec && s.head >= 0 && s.tail >= kSpan, inner = whole && s.head >= kV && s.tail >= kSpan + kV;
+        win.load(p, x, s, row, n, inner);
         float2 slope[kOut];  // first dy: outputs k and k + 8
         {
             Vec8<Tout> u[3];
+            if (inner) {
 #pragma unroll
-            for (int i = 0; i < 3; ++i) load_at(u[i], dy, s.e + i * kV, n, vec);
+                for (int i = 0; i < 3; ++i) u[i].load(dy + s.e, i * kV);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 3; ++i) load_row8(u[i], dy, s.e + i * kV, n, s.lo(i * kV), s.hi(i * kV), vec);
+            }
+            // outputs outside the row have dy = 0, and with it no part in anything
 #pragma unroll
             for (int k = 0; k < kOut; ++k) slope[k] = make_float2(u[k / kV][k % kV], u[k / kV + 1][k % kV]);
-            if (!there || s.t0 < 0 || s.t0 + kSpan + W - 1 > L) {
-                const int64_t hi = there ? L - s.t0 : 0;
-#pragma unroll
-                for (int k = 0; k < kOut; ++k) {
-                    if (k < s.lo || k >= hi) slope[k].x = 0.f;
-                    if (k + kV < s.lo || k + kV >= hi) slope[k].y = 0.f;
-                }
-            }
-            if (!there) s.hi = 0;
         }
         uint32_t m = 0;
         if constexpr (kR) m = window_starts<W, 2 * (W - 1) + kSpan>(p, b, s.t0);
@@ -372,8 +381,13 @@ __global__ void __launch_bounds__(kConvBwdThreads, 2) conv_bwd_kernel(const Conv
         float g0[kV], g1[kV];
 #pragma unroll
         for (int i = 0; i < kV; ++i) g0[i] = g[i].x, g1[i] = g[i].y;
-        store8(dx, s.e, s.lo, s.hi, vec, g0);
-        store8(dx, s.e + kV, s.lo - kV, s.hi - kV, vec, g1);
+        if (whole) {
+            store_vec(dx + s.e, g0);
+            store_vec(dx + s.e + kV, g1);
+        } else {
+            store8(dx + s.e, 0, s.lo(0), s.hi(0), vec, g0);
+            store8(dx + s.e, kV, s.lo(kV), s.hi(kV), vec, g1);
+        }
     }
     float sum[W + 1];
 #pragma unroll

@@ -17,8 +17,10 @@ using Tout = SS_INST_TOUT;
 
 template <int W>
 cudaError_t fwd(cudaStream_t s, ConvParams &p) {
-    const int64_t spans = p.batch * p.dim * ((p.L + kV - 1 + kSpan - 1) / kSpan);
+    const int64_t spans = p.batch * p.dim * spans_of(p.L);
     p.main_blocks = (spans + 255) / 256;
+    p.small = spans <= INT_MAX;
+    p.by_spans = divisor_of(spans_of(p.L)), p.by_dim = divisor_of(p.dim);
     const int64_t tail = p.last ? (p.batch * p.dim * (W - 1) + 255) / 256 : 0;
     if (p.main_blocks + tail > INT_MAX) return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)(p.main_blocks + tail);
@@ -28,10 +30,12 @@ cudaError_t fwd(cudaStream_t s, ConvParams &p) {
 }
 
 template <int W>
-cudaError_t bwd(cudaStream_t s, const ConvParams &p) {
+cudaError_t bwd(cudaStream_t s, ConvParams &p) {
     // Blocks per channel: enough for about eight blocks per SM, no more than
     // the channel's vectors feed.
-    const int64_t vecs = p.batch * ((p.L + kV - 1 + kSpan - 1) / kSpan);
+    const int64_t vecs = p.batch * spans_of(p.L);
+    p.small = vecs <= INT_MAX;
+    p.by_spans = divisor_of(spans_of(p.L));
     int nblk = 1;
     while (nblk < 8 && p.dim * nblk < (int64_t)layer_sm_count() * 8 && vecs > (int64_t)nblk * kConvBwdThreads) nblk *= 2;
     cudaLaunchConfig_t cfg{};
@@ -63,6 +67,6 @@ cudaError_t bwd(cudaStream_t s, const ConvParams &p) {
     }
 
 cudaError_t SS_CAT(conv_fwd, SS_INST_NAME)(int width, cudaStream_t s, ConvParams &p) { SS_WIDTHS(fwd) }
-cudaError_t SS_CAT(conv_bwd, SS_INST_NAME)(int width, cudaStream_t s, const ConvParams &p) { SS_WIDTHS(bwd) }
+cudaError_t SS_CAT(conv_bwd, SS_INST_NAME)(int width, cudaStream_t s, ConvParams &p) { SS_WIDTHS(bwd) }
 
 }  // namespace selscan

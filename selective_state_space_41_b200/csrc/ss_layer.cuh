@@ -79,7 +79,32 @@ struct Vec8 {
 #pragma unroll
         for (int i = 0; i < kV; ++i) put_bits(i, i >= lo && i < hi ? b[i] : 0u);
     }
+
+    // Clears all but elements [lo, hi), 0 <= lo, hi <= 8.
+    __device__ __forceinline__ void keep(int lo, int hi) {
+        const uint32_t m = ((1u << hi) - 1u) & ~((1u << lo) - 1u);
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+            if constexpr (sizeof(T) == 4) w[k] &= (uint32_t)((int)(m << (31 - k)) >> 31);
+            else w[k] &= __byte_perm((uint32_t)((int)(m << (31 - 2 * k)) >> 31), (uint32_t)((int)(m << (30 - 2 * k)) >> 31), 0x7610);
+        }
+    }
 };
+
+// The vector at element e of a tensor of n, of which elements [lo, hi) belong
+// to the row; the others are zero.  A whole vector is loaded where the tensor
+// holds it, and masked.
+template <typename T>
+__device__ __forceinline__ void load_row8(Vec8<T> &r, const T *p, int64_t e, int64_t n, int lo, int hi, bool vec) {
+    if (hi <= lo) {
+        r.clear();
+    } else if (vec && e >= 0 && e + kV <= n) {
+        r.load(p, e);
+        if (lo > 0 || hi < kV) r.keep(lo, hi);
+    } else {
+        r.load_part(p, e, lo, hi);
+    }
+}
 
 // The vector at element e, of which [lo, hi) may be read.
 template <typename T>
@@ -139,6 +164,22 @@ __device__ __forceinline__ void sigmoid2(float v, float &s, float &c) {
     s = v >= 0.f ? r : q;
     c = v >= 0.f ? q : r;
 }
+
+// Division of n < 2^31 by a fixed d: n mul >> (32 + shift), with
+// 2^(32 + shift) >= 2^31 d and mul its quotient by d rounded up: the excess
+// mul d - 2^(32 + shift) is below d, so n times it stays below the power.
+struct Divisor {
+    uint32_t d, mul;
+    int shift;
+};
+inline Divisor divisor_of(int64_t d) {
+    Divisor r{(uint32_t)d, 0u, 0};
+    if (d <= 1) return r;
+    while (((int64_t)1 << (r.shift + 1)) < d) ++r.shift;  // 2^(shift + 1) >= d
+    r.mul = (uint32_t)((((uint64_t)1 << (32 + r.shift)) + (uint64_t)d - 1) / (uint64_t)d);
+    return r;
+}
+__device__ __forceinline__ uint32_t divide(uint32_t n, const Divisor &v) { return v.mul ? __umulhi(n, v.mul) >> v.shift : n; }
 
 // Bit i: whether byte i of the pair of words is nonzero.
 __device__ __forceinline__ uint32_t nonzero_bytes(uint32_t lo, uint32_t hi) {
