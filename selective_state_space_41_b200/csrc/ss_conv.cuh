@@ -147,6 +147,18 @@ struct Window {
         if (k >= kV) v[k - kV].y = f;
     }
     __device__ __forceinline__ float get(int k) const { return k < kPairs ? v[k].x : v[k - kV].y; }
+    // From its vectors, the one before the thread's steps first.
+    __device__ __forceinline__ void take(const ConvParams &p, const Vec8<T> (&q)[kVecs + 1], const Span &s, int64_t row) {
+#pragma unroll
+        for (int k = 0; k < kN; ++k) set(k, q[(k + kV - (W - 1)) / kV][(k + kV - (W - 1)) % kV]);
+        if (p.h0 && s.head < W - 1) {
+#pragma unroll
+            for (int k = 0; k < 2 * (W - 1) + kV - 1 && k < kN; ++k) {  // head >= -7: steps -(W-1) .. -1 lie here
+                const int t = s.head - (W - 1) + k;
+                if (t < 0 && t >= -(W - 1)) set(k, load_elem(static_cast<const T *>(p.h0), row * (W - 1) + (W - 1) + t));
+            }
+        }
+    }
     // inner: all of its vectors lie in the row and are whole
     __device__ __forceinline__ void load(const ConvParams &p, const T *x, const Span &s, int64_t row, int64_t n, bool inner) {
         Vec8<T> q[kVecs + 1];
@@ -158,15 +170,7 @@ struct Window {
             for (int i = 0; i <= kVecs; ++i)
                 load_row8(q[i], x, s.e + (i - 1) * kV, n, s.lo((i - 1) * kV), s.hi((i - 1) * kV), p.vec);
         }
-#pragma unroll
-        for (int k = 0; k < kN; ++k) set(k, q[(k + kV - (W - 1)) / kV][(k + kV - (W - 1)) % kV]);
-        if (p.h0 && s.head < W - 1) {
-#pragma unroll
-            for (int k = 0; k < 2 * (W - 1) + kV - 1 && k < kN; ++k) {  // head >= -7: steps -(W-1) .. -1 lie here
-                const int t = s.head - (W - 1) + k;
-                if (t < 0 && t >= -(W - 1)) set(k, load_elem(static_cast<const T *>(p.h0), row * (W - 1) + (W - 1) + t));
-            }
-        }
+        take(p, q, s, row);
     }
 };
 
@@ -261,10 +265,52 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(const ConvParams p) {
     }
 }
 
-constexpr int kConvBwdThreads = 256;
+constexpr int kConvBwdThreads = 128;
+
+// The backward's next spans, copied in while the present ones are worked on:
+// a slot for each thread's 16 elements of a tensor, and one on either side.
+template <typename T>
+struct Slots {
+    static constexpr int kQ = sizeof(T) / 2;  // 16-byte words of a vector
+    uint4 w[(kConvBwdThreads + 2) * 2 * kQ];
+    // Both vectors of a thread whose steps all lie in the row.
+    __device__ __forceinline__ void fill_whole(int t, const T *p) {
+#pragma unroll
+        for (int k = 0; k < 2 * kQ; ++k) cp_async16(w + (t + 1) * 2 * kQ + k, p + k * (16 / sizeof(T)));
+    }
+    // Vector i of the tensor's spans, counted from the slot before thread 0's.
+    __device__ __forceinline__ void fill(int i, const T *p, int64_t e, int64_t n, int lo, int hi, bool vec) {
+        uint4 *to = w + i * kQ;
+        if (hi > lo && vec && e >= 0 && e + kV <= n) {
+#pragma unroll
+            for (int k = 0; k < kQ; ++k) cp_async16(to + k, p + e + k * (16 / sizeof(T)));
+        } else if (hi > lo) {
+            Vec8<T> v;
+            v.load_part(p, e, lo, hi);
+#pragma unroll
+            for (int k = 0; k < kQ; ++k) to[k] = make_uint4(v.w[4 * k], v.w[4 * k + 1], v.w[4 * k + 2], v.w[4 * k + 3]);
+        }
+    }
+    // It, with elements [lo, hi) kept (the others were not copied, or are
+    // those of a neighbouring row).
+    __device__ __forceinline__ void read(Vec8<T> &v, int i) const {
+#pragma unroll
+        for (int k = 0; k < kQ; ++k) {
+            const uint4 u = w[i * kQ + k];
+            v.w[4 * k] = u.x, v.w[4 * k + 1] = u.y, v.w[4 * k + 2] = u.z, v.w[4 * k + 3] = u.w;
+        }
+    }
+    __device__ __forceinline__ void read(Vec8<T> &v, int i, int lo, int hi) const {
+        read(v, i);
+        if (lo > 0 || hi < kV) {
+            if (hi > lo) v.keep(lo, hi);
+            else v.clear();
+        }
+    }
+};
 
 template <typename Tin, typename Tout, int W, bool kR>
-__global__ void __launch_bounds__(kConvBwdThreads, 2) conv_bwd_kernel(const ConvParams p, int nblk) {
+__global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const ConvParams p, int nblk) {
     constexpr bool kFast = sizeof(Tin) == 2;
     const int64_t L = p.L, n = p.batch * p.dim * L;
     const int64_t d = blockIdx.x / nblk;  // the blocks of a channel follow one another: one cluster
@@ -282,32 +328,77 @@ __global__ void __launch_bounds__(kConvBwdThreads, 2) conv_bwd_kernel(const Conv
 #pragma unroll
     for (int j = 0; j <= W; ++j) sum2[j] = both(0.f);
 
+    __shared__ Slots<Tin> xs[2];
+    __shared__ Slots<Tout> gs[2];
+    const int t = threadIdx.x;
     const int64_t nv = spans_of(L), total = p.batch * nv, stride = (int64_t)nblk * blockDim.x;
-    for (int64_t q0 = (int64_t)rank * blockDim.x; q0 < total; q0 += stride) {
-        const int64_t q = q0 + threadIdx.x;
+    // Span q of the channel; one behind the last has no step.
+    const auto place = [&](int64_t q, int64_t &b) {
         const bool there = q < total;
-        const int64_t b = !there ? 0 : p.small ? (int64_t)divide((uint32_t)q, p.by_spans) : q / nv;
+        b = !there ? 0 : p.small ? (int64_t)divide((uint32_t)q, p.by_spans) : q / nv;
+        Span s = span_of((b * p.dim + d) * L, there ? q - b * nv : 0, L);
+        if (!there) s.tail = -kSpan;
+        return s;
+    };
+    const auto fill = [&](int64_t q, int buf) {
+        int64_t b;
+        const Span s = place(q, b);
+        if (vec && s.head >= 0 && s.tail >= kSpan) {
+            xs[buf].fill_whole(t, x + s.e);
+            gs[buf].fill_whole(t, dy + s.e);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                xs[buf].fill(2 * t + 2 + i, x, s.e + i * kV, n, s.lo(i * kV), s.hi(i * kV), vec);
+                gs[buf].fill(2 * t + 2 + i, dy, s.e + i * kV, n, s.lo(i * kV), s.hi(i * kV), vec);
+            }
+        }
+        if (t == 0) xs[buf].fill(1, x, s.e - kV, n, s.lo(-kV), s.hi(-kV), vec);
+        if (t == kConvBwdThreads - 1) {
+            xs[buf].fill(2 * t + 4, x, s.e + kSpan, n, s.lo(kSpan), s.hi(kSpan), vec);
+            gs[buf].fill(2 * t + 4, dy, s.e + kSpan, n, s.lo(kSpan), s.hi(kSpan), vec);
+        }
+        cp_async_commit();
+    };
+    int buf = 0;
+    fill((int64_t)rank * blockDim.x + t, 0);
+    for (int64_t q0 = (int64_t)rank * blockDim.x; q0 < total; q0 += stride, buf ^= 1) {
+        const int64_t q = q0 + t;
+        const bool there = q < total;
+        if (q0 + stride < total) {
+            fill(q + stride, buf ^ 1);
+            cp_async_wait_one();
+        } else {
+            cp_async_wait_all();
+        }
+        __syncthreads();
+        int64_t b;
+        const Span s = place(q, b);
         const int64_t row = b * p.dim + d;
-        Span s = span_of(row * L, there ? q - b * nv : 0, L);
+        const bool whole = vec && s.head >= 0 && s.tail >= kSpan;
         constexpr int kOut = kV + W - 1;  // pairs of outputs: the thread's steps and W - 1 behind
         Window<Tin, W, 3> win;
-        if (!there) s.tail = -kSpan;
-        const bool whole = vec && s.head >= 0 && s.tail >= kSpan, inner = whole && s.head >= kV && s.tail >= kSpan + kV;
-        win.load(p, x, s, row, n, inner);
         float2 slope[kOut];  // first dy: outputs k and k + 8
         {
+            Vec8<Tin> v[4];
             Vec8<Tout> u[3];
-            if (inner) {
+            if (s.head >= kV && s.tail >= kSpan + kV) {
 #pragma unroll
-                for (int i = 0; i < 3; ++i) u[i].load(dy + s.e, i * kV);
+                for (int i = 0; i < 4; ++i) xs[buf].read(v[i], 2 * t + 1 + i);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) gs[buf].read(u[i], 2 * t + 2 + i);
             } else {
 #pragma unroll
-                for (int i = 0; i < 3; ++i) load_row8(u[i], dy, s.e + i * kV, n, s.lo(i * kV), s.hi(i * kV), vec);
+                for (int i = 0; i < 4; ++i) xs[buf].read(v[i], 2 * t + 1 + i, s.lo((i - 1) * kV), s.hi((i - 1) * kV));
+#pragma unroll
+                for (int i = 0; i < 3; ++i) gs[buf].read(u[i], 2 * t + 2 + i, s.lo(i * kV), s.hi(i * kV));
             }
+            win.take(p, v, s, row);
             // outputs outside the row have dy = 0, and with it no part in anything
 #pragma unroll
             for (int k = 0; k < kOut; ++k) slope[k] = make_float2(u[k / kV][k % kV], u[k / kV + 1][k % kV]);
         }
+        __syncthreads();  // this half may be filled again
         uint32_t m = 0;
         if constexpr (kR) m = window_starts<W, 2 * (W - 1) + kSpan>(p, b, s.t0);
         const bool cutting = kR && __any_sync(0xffffffffu, m != 0);
