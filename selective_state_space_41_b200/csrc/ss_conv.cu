@@ -18,9 +18,9 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvParams p) {
     const float *w = p.weight + d * W;
     float v[kMaxWidth - 1], wv[kMaxWidth];
 #pragma unroll
-    for (int j = 0; j < kMaxWidth - 1; ++j) v[j] = j < W - 1 ? static_cast<float>(state[j]) : 0.f;
+    for (int j = 0; j < kMaxWidth - 1; ++j) v[j] = static_cast<float>(state[min(j, W - 2)]);  // all in flight at once
 #pragma unroll
-    for (int j = 0; j < kMaxWidth; ++j) wv[j] = j < W ? __ldg(w + j) : 0.f;
+    for (int j = 0; j < kMaxWidth; ++j) wv[j] = __ldg(w + min(j, W - 1));
     const float xv = load_elem(static_cast<const Tin *>(p.x), row);
     float acc = p.bias ? __ldg(p.bias + d) : 0.f;
 #pragma unroll

@@ -6,18 +6,20 @@
 //   y_t = h_t or h_t silu(z_t)
 //
 // One state per row (b, d), so a step costs two or three reads and a write
-// and some twenty operations: the kernels are bound by memory, and what the
-// design has to do is to keep enough loads in flight and the serial chain of
-// the recurrence short.  A warp takes 256 steps of a row at a time, eight per
-// lane.  Each lane folds its steps into one pair (A, B): the map h -> A h + B
-// of its eight steps.  The pairs compose as (A2, B2) o (A1, B1) = (A2 A1,
-// A2 B1 + B2), so five shuffle rounds give every lane the map of all lanes
-// before it; applied to the state entering the 256 steps it gives the state
-// entering the lane's own, from which the lane runs its steps again, now one
-// after the other as the formula has them.  W warps share a row when there
-// are few rows: each folds its own 256 steps, and W pairs in shared memory
-// join them.  The loads of the next piece are issued before the current one
-// is worked on.
+// and some twenty operations: the kernels are bound by memory, and close
+// behind it by the instructions they issue.  What the design has to do is to
+// keep enough loads in flight, the serial chain of the recurrence short and
+// the work per step small.  G lanes take a row (32, or fewer for short rows),
+// 16 steps each at a time forward and 8 backward.  Each lane folds its steps
+// into one pair (A, B): the map h -> A h + B.  The pairs compose as
+// (A2, B2) o (A1, B1) = (A2 A1, A2 B1 + B2), so log2 G shuffle rounds give
+// every lane the map of all lanes before it; applied to the state entering
+// the G lanes' steps it gives the state entering the lane's own, from which
+// the lane runs its steps again, now one after the other as the formula has
+// them.  W warps share a row when there are few rows: each folds its own
+// steps, and W pairs in shared memory join them.  The loads of the next steps
+// are issued before the current ones are worked on; gates and products are
+// computed in pairs of steps with the packed arithmetic of two floats.
 //
 // Sequence starts cut the maps: behind a start the entering state does not
 // count, whatever it is (an infinity or a NaN of another sequence included),
@@ -37,8 +39,8 @@
 namespace selscan {
 namespace {
 
-constexpr int kPiece = 256;   // steps a warp takes at a time; also the checkpoint stride
-constexpr int kMaxWarps = 16; // warps sharing a row
+constexpr int kPiece = 256;    // steps between two checkpoints of a row
+constexpr int kMaxWarps = 16;  // warps sharing a row
 
 struct GlrParams {
     const void *x, *g, *z, *dy;
@@ -52,42 +54,69 @@ struct GlrParams {
     int sigmoid, couple, vec;
 };
 
-// a, 1 - a of a step's gate input.
+// a, 1 - a of two gate inputs.  Fast: e = exp(-g) with its exponent held
+// below 2^126 (a NaN passes), so 1 / (1 + e) and e / (1 + e) are both finite
+// and each has its full relative precision.
 template <bool kFast>
-__device__ __forceinline__ void gate(float g, bool sigmoid, float &a, float &keep) {
-    if (sigmoid) {
-        sigmoid2<kFast>(g, a, keep);
-    } else {
+__device__ __forceinline__ void gate2(float2 g, bool sigmoid, float2 &a, float2 &keep) {
+    if (!sigmoid) {
         a = g;
-        keep = 1.f - g;
+        keep = add2(both(1.f), neg2(g));
+    } else if constexpr (kFast) {
+        float2 t = mul2(g, both(-kLog2e));
+        asm("min.NaN.f32 %0, %1, %2;" : "=f"(t.x) : "f"(t.x), "f"(126.f));
+        asm("min.NaN.f32 %0, %1, %2;" : "=f"(t.y) : "f"(t.y), "f"(126.f));
+        const float2 e = make_float2(sfu_exp2(t.x), sfu_exp2(t.y)), u = add2(e, both(1.f));
+        a = make_float2(sfu_rcp(u.x), sfu_rcp(u.y));
+        keep = mul2(e, a);
+    } else {
+        sigmoid2<false>(g.x, a.x, keep.x);
+        sigmoid2<false>(g.y, a.y, keep.y);
     }
 }
 
-// Lanes lane-d+1 .. lane as a mask (the lanes a pair stands for before the
-// shuffle round of distance d), and lane .. lane+d-1.
+// z sigmoid(z).
+template <bool kFast>
+__device__ __forceinline__ float2 gated2(float2 z) {
+    if constexpr (kFast) {
+        const float2 t = mul2(z, both(-kLog2e)), u = add2(make_float2(sfu_exp2(t.x), sfu_exp2(t.y)), both(1.f));
+        return mul2(z, make_float2(sfu_rcp(u.x), sfu_rcp(u.y)));
+    } else {
+        return make_float2(z.x / (1.f + expf(-z.x)), z.y / (1.f + expf(-z.y)));
+    }
+}
+
+// The lanes that a pair stands for before the shuffle round of distance d:
+// lane-d+1 .. lane, and lane .. lane+d-1, as masks.
 __device__ __forceinline__ uint32_t lanes_up_to(int lane, int d) { return ((1u << d) - 1u) << (lane - d + 1); }
 __device__ __forceinline__ uint32_t lanes_from(int lane, int d) { return ((1u << d) - 1u) << lane; }
 
-// Inclusive composition over lanes 0..lane.  cuts: lanes that hold a start.
-template <bool kR>
-__device__ __forceinline__ void scan_up(float &A, float &B, int lane, uint32_t cuts) {
+// Inclusive composition over the row's lanes up to this one.  G: its lanes
+// (kG of them, or `lanes` where kG is 0); cuts: lanes that hold a start.
+template <bool kR, int kG>
+__device__ __forceinline__ void scan_up(float &A, float &B, int lane, int lanes, uint32_t cuts) {
+    const int G = kG ? kG : lanes, in = lane & (G - 1);
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
+        if (d >= G) break;
         const float Ao = __shfl_up_sync(0xffffffffu, A, d), Bo = __shfl_up_sync(0xffffffffu, B, d);
-        if (lane >= d && !(kR && (cuts & lanes_up_to(lane, d)))) {
+        if (in >= d && !(kR && (cuts & lanes_up_to(lane, d)))) {
             B = fmaf(A, Bo, B);
             A *= Ao;
         }
     }
 }
 
-// Inclusive composition over lanes 31..lane (the adjoint's direction).
-template <bool kR>
-__device__ __forceinline__ void scan_down(float &A, float &B, int lane, uint32_t cuts) {
+// Inclusive composition over the row's lanes from the last to this one (the
+// adjoint's direction).
+template <bool kR, int kG>
+__device__ __forceinline__ void scan_down(float &A, float &B, int lane, int lanes, uint32_t cuts) {
+    const int G = kG ? kG : lanes, in = lane & (G - 1);
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
+        if (d >= G) break;
         const float Ao = __shfl_down_sync(0xffffffffu, A, d), Bo = __shfl_down_sync(0xffffffffu, B, d);
-        if (lane + d < 32 && !(kR && (cuts & lanes_from(lane, d)))) {
+        if (in + d < G && !(kR && (cuts & lanes_from(lane, d)))) {
             B = fmaf(A, Bo, B);
             A *= Ao;
         }
@@ -99,197 +128,281 @@ struct Pair {
     int cut;
 };
 
-// kMulti: one warp per row, several rows per block; otherwise the block's
-// warps share its row.
-template <typename Tin, typename Tout, bool kZ, bool kR, bool kMulti>
-__global__ void __launch_bounds__(512) glr_fwd_kernel(const GlrParams p) {
-    constexpr bool kFast = sizeof(Tin) == 2;
-    __shared__ Pair pairs[2][kMaxWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int W = kMulti ? 1 : warps, w = kMulti ? 0 : warp;
-    const int64_t row = kMulti ? (int64_t)blockIdx.x * warps + warp : blockIdx.x;
-    if (row >= p.rows) return;  // a whole warp of a kMulti block, which has no barrier
-    const int64_t e0 = row * p.L;
-    const int shift = (int)(e0 & (kV - 1));
-    const int64_t base = e0 - shift, steps = shift + p.L;
-    const int64_t bl = kR ? row / p.dim * p.L - shift : 0, bl_all = kR ? p.rows / p.dim * p.L : 0;
-    const Tin *x = static_cast<const Tin *>(p.x), *g = static_cast<const Tin *>(p.g), *z = static_cast<const Tin *>(p.z);
-    Tout *y = static_cast<Tout *>(p.y);
-    const bool vec = p.vec, sigmoid = p.sigmoid, couple = p.couple;
+// Where a row lies, in virtual steps from the 8-element boundary before it.
+struct Row {
+    int64_t row, base, steps;
+    int shift;
+    bool there;
+};
+template <bool kShared>
+__device__ __forceinline__ Row row_of(const GlrParams &p, int lanes) {
+    Row r;
+    const int per = kShared ? 1 : (int)blockDim.x / lanes;  // rows of a block
+    r.row = kShared ? blockIdx.x : (int64_t)blockIdx.x * per + (int)threadIdx.x / lanes;
+    r.there = r.row < p.rows;
+    if (!r.there) r.row = p.rows - 1;  // lanes that only take part in their warp's shuffles
+    const int64_t e0 = r.row * p.L;
+    r.shift = (int)(e0 & (kV - 1));
+    r.base = e0 - r.shift;
+    r.steps = r.shift + p.L;
+    return r;
+}
 
-    Vec8<Tin> nx, ng, nz;
+// Steps [lo, hi) of the kV at virtual step v that are the row's.
+__device__ __forceinline__ void bounds_of(const Row &r, int64_t v, int &lo, int &hi) {
+    const int64_t left = r.steps - v;
+    lo = v == 0 ? r.shift : 0;
+    hi = left >= kV ? kV : left > 0 ? (int)left : 0;
+}
+
+// kShared: the block's warps share a row; otherwise every kG lanes (kG 0:
+// `lanes`) have a row of their own.
+template <typename Tin, typename Tout, bool kZ, bool kR, bool kShared, int kG>
+__global__ void __launch_bounds__(512) glr_fwd_kernel(const GlrParams p, int lanes) {
+    constexpr bool kFast = sizeof(Tin) == 2;
+    constexpr int kVecs = 2, kE = kVecs * kV;  // steps of a lane
+    __shared__ Pair pairs[2][kMaxWarps];
+    const int G = kG ? kG : lanes, lane = threadIdx.x & 31, in = lane & (G - 1);
+    const int W = kShared ? (int)blockDim.x >> 5 : 1, w = kShared ? (int)threadIdx.x >> 5 : 0;
+    const Row r = row_of<kShared>(p, G);
+    const int64_t bl = kR ? r.row / p.dim * p.L - r.shift : 0, bl_all = kR ? p.rows / p.dim * p.L : 0;
+    const Tin *x = static_cast<const Tin *>(p.x) + r.base, *g = static_cast<const Tin *>(p.g) + r.base;
+    const Tin *z = kZ ? static_cast<const Tin *>(p.z) + r.base : nullptr;
+    Tout *y = static_cast<Tout *>(p.y) + r.base;
+    const bool vec = p.vec, sigmoid = p.sigmoid, couple = p.couple;
+    const int64_t span = (int64_t)G * kE, stride = W * span;  // steps of the row's lanes in a warp, in the block
+
+    Vec8<Tin> nx[kVecs], ng[kVecs], nz[kVecs];
     uint32_t ncut = 0;
     const auto fetch = [&](int64_t v) {
-        const int lo = clamp8(shift - v), hi = clamp8(steps - v);
-        load8(ng, g, base + v, lo, hi, vec);
-        load8(nx, x, base + v, lo, hi, vec);
-        if constexpr (kZ) load8(nz, z, base + v, lo, hi, vec);
-        if constexpr (kR) ncut = start_bits(p.reset, bl + v, bl_all, lo, hi);
+        ncut = 0;
+        if (vec && v > 0 && v + kE <= r.steps) {
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) {
+                ng[k].load(g, v + k * kV);
+                nx[k].load(x, v + k * kV);
+                if constexpr (kZ) nz[k].load(z, v + k * kV);
+                if constexpr (kR) ncut |= start_bits(p.reset, bl + v + k * kV, bl_all, 0, kV) << (k * kV);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) {
+                int lo, hi;
+                bounds_of(r, v + k * kV, lo, hi);
+                load8(ng[k], g, v + k * kV, lo, hi, vec);
+                load8(nx[k], x, v + k * kV, lo, hi, vec);
+                if constexpr (kZ) load8(nz[k], z, v + k * kV, lo, hi, vec);
+                if constexpr (kR) ncut |= start_bits(p.reset, bl + v + k * kV, bl_all, lo, hi) << (k * kV);
+            }
+        }
     };
 
-    float carry = p.h0 ? p.h0[row] : 0.f;
+    float carry = p.h0 ? p.h0[r.row] : 0.f;
     int buf = 0;
-    fetch((int64_t)w * kPiece + lane * kV);
-    for (int64_t v0 = 0; v0 < steps; v0 += (int64_t)W * kPiece, buf ^= 1) {
-        const int64_t v = v0 + (int64_t)w * kPiece + lane * kV;
-        const int lo = clamp8(shift - v), hi = clamp8(steps - v);
-        float a[kV], b[kV];
+    const int64_t mine = w * span + (int64_t)in * kE;
+    // (rows that share a warp have one turn, whatever their shifts: glr_shape)
+    fetch(mine);
+    for (int64_t v0 = 0; v0 < r.steps; v0 += stride, buf ^= 1) {
+        const int64_t v = v0 + mine;
+        float a[kE], b[kE];
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            float keep;
-            gate<kFast>(ng[i], sigmoid, a[i], keep);
-            b[i] = couple ? keep * nx[i] : nx[i];
+        for (int i = 0; i < kE; i += 2) {
+            float2 a2, k2, b2 = nx[i / kV].pair(i % kV / 2);
+            gate2<kFast>(ng[i / kV].pair(i % kV / 2), sigmoid, a2, k2);
+            if (couple) b2 = mul2(k2, b2);
+            a[i] = a2.x, a[i + 1] = a2.y, b[i] = b2.x, b[i + 1] = b2.y;
         }
-        if (lo > 0 || hi < kV) {
+        const bool inner = v > 0 && v + kE <= r.steps;  // all of the lane's steps are the row's
+        if (!inner) {
 #pragma unroll
-            for (int i = 0; i < kV; ++i)
-                if (i < lo || i >= hi) a[i] = 1.f, b[i] = 0.f;
+            for (int k = 0; k < kVecs; ++k) {
+                int lo, hi;
+                bounds_of(r, v + k * kV, lo, hi);
+#pragma unroll
+                for (int i = 0; i < kV; ++i)
+                    if (i < lo || i >= hi) a[k * kV + i] = 1.f, b[k * kV + i] = 0.f;
+            }
         }
-        const Vec8<Tin> cz = nz;
+        Vec8<Tin> cz[kVecs];
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) cz[k] = nz[k];
         const uint32_t cut = ncut;
-        if (v0 + (int64_t)W * kPiece < steps) fetch(v + (int64_t)W * kPiece);
+        if (v0 + stride < r.steps) fetch(v + stride);
 
         // the lane's map, then the maps of the lanes before it
         float A = 1.f, B = 0.f;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
+        for (int i = 0; i < kE; ++i) {
             const bool c = kR && (cut >> i & 1u);
             B = c ? b[i] : fmaf(a[i], B, b[i]);
             A = c ? 0.f : A * a[i];
         }
         const uint32_t cuts = kR ? __ballot_sync(0xffffffffu, cut != 0) : 0u;
-        scan_up<kR>(A, B, lane, cuts);
-        const float Aw = __shfl_sync(0xffffffffu, A, 31), Bw = __shfl_sync(0xffffffffu, B, 31);
+        scan_up<kR, kG>(A, B, lane, lanes, cuts);
+        const int last = lane | (G - 1);  // the row's last lane in the warp
+        const uint32_t row_cuts = kR ? cuts & lanes_up_to(last, G == 32 ? 31 : G) : 0u;
+        const bool any = kR && (G == 32 ? cuts != 0 : row_cuts != 0);
+        const float Aw = __shfl_sync(0xffffffffu, A, last), Bw = __shfl_sync(0xffffffffu, B, last);
         float Ax = __shfl_up_sync(0xffffffffu, A, 1), Bx = __shfl_up_sync(0xffffffffu, B, 1);
-        if (lane == 0) Ax = 1.f, Bx = 0.f;
+        if (in == 0) Ax = 1.f, Bx = 0.f;
 
-        float in = carry;  // the state entering this warp's piece
-        if constexpr (kMulti) {
-            carry = kR && cuts ? Bw : fmaf(Aw, carry, Bw);
-        } else {
-            if (lane == 0) pairs[buf][w] = {Aw, Bw, kR && cuts ? 1 : 0};
+        float from = carry;  // the state entering this warp's steps
+        if constexpr (kShared) {
+            if (lane == 0) pairs[buf][w] = {Aw, Bw, any ? 1 : 0};
             __syncthreads();
             float c = carry;
             for (int k = 0; k < W; ++k) {
-                if (k == w) in = c;
+                if (k == w) from = c;
                 const Pair q = pairs[buf][k];
                 c = kR && q.cut ? q.B : fmaf(q.A, c, q.B);
             }
             carry = c;
+        } else {
+            carry = any ? Bw : fmaf(Aw, carry, Bw);
         }
-        const int64_t piece = v0 / kPiece + w;
-        if (p.ckpt && lane == 0 && piece * kPiece < steps) p.ckpt[row * p.nck + piece] = in;
-        float h = kR && (cuts & ((1u << lane) - 1u)) ? Bx : fmaf(Ax, in, Bx);
+        float h = kR && in > 0 && (cuts & lanes_up_to(lane - 1, in)) ? Bx : fmaf(Ax, from, Bx);
+        if (p.ckpt && v % kPiece == 0 && v < r.steps && r.there) p.ckpt[r.row * p.nck + v / kPiece] = h;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
+        for (int i = 0; i < kE; ++i) {
             h = kR && (cut >> i & 1u) ? b[i] : fmaf(a[i], h, b[i]);
             b[i] = h;
         }
-        if (y) {
-            if constexpr (kZ) {
+        if (!p.y || !r.there) continue;
 #pragma unroll
-                for (int i = 0; i < kV; ++i) {
-                    float s, c;
-                    sigmoid2<kFast>(cz[i], s, c);
-                    b[i] *= cz[i] * s;
-                }
+        for (int k = 0; k < kVecs; ++k) {
+            float o[kV];
+#pragma unroll
+            for (int i = 0; i < kV; i += 2) {
+                float2 h2 = make_float2(b[k * kV + i], b[k * kV + i + 1]);
+                if constexpr (kZ) h2 = mul2(h2, gated2<kFast>(cz[k].pair(i / 2)));
+                o[i] = h2.x, o[i + 1] = h2.y;
             }
-            store8(y, base + v, lo, hi, vec, b);
+            if (inner && vec) {
+                store_vec(y + v + k * kV, o);
+            } else {
+                int lo, hi;
+                bounds_of(r, v + k * kV, lo, hi);
+                store8(y, v + k * kV, lo, hi, vec, o);
+            }
         }
     }
-    if (p.last && lane == 0 && w == 0) p.last[row] = carry;
+    if (p.last && r.there && in == 0 && w == 0) p.last[r.row] = carry;
 }
 
-template <typename Tin, typename Tout, bool kZ, bool kR, bool kMulti>
-__global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p) {
+template <typename Tin, typename Tout, bool kZ, bool kR, bool kShared, int kG>
+__global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p, int lanes) {
     constexpr bool kFast = sizeof(Tin) == 2;
     __shared__ Pair pairs[2][kMaxWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int W = kMulti ? 1 : warps, w = kMulti ? 0 : warp;
-    const int64_t row = kMulti ? (int64_t)blockIdx.x * warps + warp : blockIdx.x;
-    if (row >= p.rows) return;
-    const int64_t e0 = row * p.L;
-    const int shift = (int)(e0 & (kV - 1));
-    const int64_t base = e0 - shift, steps = shift + p.L;
-    const int64_t bl = kR ? row / p.dim * p.L - shift : 0, bl_all = kR ? p.rows / p.dim * p.L : 0;
-    const Tin *x = static_cast<const Tin *>(p.x), *g = static_cast<const Tin *>(p.g), *z = static_cast<const Tin *>(p.z);
-    const Tout *dy = static_cast<const Tout *>(p.dy);
+    const int G = kG ? kG : lanes, lane = threadIdx.x & 31, in = lane & (G - 1);
+    const int W = kShared ? (int)blockDim.x >> 5 : 1, w = kShared ? (int)threadIdx.x >> 5 : 0;
+    const Row r = row_of<kShared>(p, G);
+    const int64_t bl = kR ? r.row / p.dim * p.L - r.shift : 0, bl_all = kR ? p.rows / p.dim * p.L : 0;
+    const Tin *x = static_cast<const Tin *>(p.x) + r.base, *g = static_cast<const Tin *>(p.g) + r.base;
+    const Tin *z = kZ ? static_cast<const Tin *>(p.z) + r.base : nullptr;
+    const Tout *dy = static_cast<const Tout *>(p.dy) + r.base;
+    Tin *dx = static_cast<Tin *>(p.dx) + r.base, *dg = static_cast<Tin *>(p.dg) + r.base;
+    Tin *dz = kZ ? static_cast<Tin *>(p.dz) + r.base : nullptr;
+    const float *ckpt = p.ckpt_in + r.row * p.nck;
     const bool vec = p.vec, sigmoid = p.sigmoid, couple = p.couple;
+    const int64_t span = (int64_t)G * kV, stride = W * span;  // (span divides kPiece: one checkpoint a span)
 
     Vec8<Tin> nx, ng, nz;
     Vec8<Tout> nd;
     uint32_t ncut = 0;
     float nin = 0.f;
-    const auto fetch = [&](int64_t v) {
-        const int lo = clamp8(shift - v), hi = clamp8(steps - v);
-        load8(ng, g, base + v, lo, hi, vec);
-        load8(nx, x, base + v, lo, hi, vec);
-        load8(nd, dy, base + v, lo, hi, vec);
-        if constexpr (kZ) load8(nz, z, base + v, lo, hi, vec);
-        if constexpr (kR) ncut = start_bits(p.reset, bl + v, bl_all, lo, hi);
-        const int64_t piece = v / kPiece;
-        nin = piece * kPiece < steps ? __ldg(p.ckpt_in + row * p.nck + piece) : 0.f;
+    const auto fetch = [&](int64_t v, int64_t start) {  // the lane's steps, and where the row's lanes begin
+        if (vec && v > 0 && v + kV <= r.steps) {
+            ng.load(g, v);
+            nx.load(x, v);
+            nd.load(dy, v);
+            if constexpr (kZ) nz.load(z, v);
+            if constexpr (kR) ncut = start_bits(p.reset, bl + v, bl_all, 0, kV);
+        } else {
+            int lo, hi;
+            bounds_of(r, v, lo, hi);
+            load8(ng, g, v, lo, hi, vec);
+            load8(nx, x, v, lo, hi, vec);
+            load8(nd, dy, v, lo, hi, vec);
+            if constexpr (kZ) load8(nz, z, v, lo, hi, vec);
+            if constexpr (kR) ncut = start_bits(p.reset, bl + v, bl_all, lo, hi);
+        }
+        nin = start < r.steps ? __ldg(ckpt + start / kPiece) : 0.f;
     };
 
-    const int64_t stride = (int64_t)W * kPiece;
-    float carry = p.dlast ? p.dlast[row] : 0.f;
+    float carry = p.dlast ? p.dlast[r.row] : 0.f;
     int buf = 0;
-    int64_t v0 = (steps - 1) / stride * stride;
-    fetch(v0 + (int64_t)w * kPiece + lane * kV);
+    int64_t v0 = (r.steps - 1) / stride * stride;
+    fetch(v0 + w * span + in * kV, v0 + w * span);
     for (; v0 >= 0; v0 -= stride, buf ^= 1) {
-        const int64_t v = v0 + (int64_t)w * kPiece + lane * kV;
-        const int lo = clamp8(shift - v), hi = clamp8(steps - v);
-        const Vec8<Tin> cx = nx, cz = nz, cg = ng;
-        const Vec8<Tout> cd = nd;
-        const uint32_t cut = ncut;
-        const float in = nin;
-        if (v0 > 0) fetch(v - stride);
-
-        float a[kV], keep[kV];
+        const int64_t v = v0 + w * span + in * kV;
+        const bool inner = v > 0 && v + kV <= r.steps;
+        float2 a[kV / 2], keep[kV / 2];
 #pragma unroll
-        for (int i = 0; i < kV; ++i) gate<kFast>(cg[i], sigmoid, a[i], keep[i]);
-        if (lo > 0 || hi < kV) {
+        for (int i = 0; i < kV / 2; ++i) gate2<kFast>(ng.pair(i), sigmoid, a[i], keep[i]);
+        if (!inner) {
+            int lo, hi;
+            bounds_of(r, v, lo, hi);
 #pragma unroll
-            for (int i = 0; i < kV; ++i)
-                if (i < lo || i >= hi) a[i] = 1.f, keep[i] = 0.f;
+            for (int i = 0; i < kV / 2; ++i) {
+                if (2 * i < lo || 2 * i >= hi) a[i].x = 1.f, keep[i].x = 0.f;
+                if (2 * i + 1 < lo || 2 * i + 1 >= hi) a[i].y = 1.f, keep[i].y = 0.f;
+            }
         }
-        // the state entering the lane's steps; masked steps have zero inputs
-        float A = 1.f, B = 0.f;
+        // masked steps have inputs of zero
+        float2 xv[kV / 2], b[kV / 2], dh[kV / 2], dzv[kV / 2];
+#pragma unroll
+        for (int i = 0; i < kV / 2; ++i) {
+            xv[i] = nx.pair(i);
+            b[i] = couple ? mul2(keep[i], xv[i]) : xv[i];
+            dh[i] = nd.pair(i);
+            if constexpr (kZ) {
+                // dy silu(z) and dy silu'(z) = dy s (1 + z (1 - s))
+                const float2 zv = nz.pair(i);
+                float2 s;
+                if constexpr (kFast) {
+                    const float2 t = mul2(zv, both(-kLog2e)), u = add2(make_float2(sfu_exp2(t.x), sfu_exp2(t.y)), both(1.f));
+                    s = make_float2(sfu_rcp(u.x), sfu_rcp(u.y));
+                } else {
+                    s = make_float2(1.f / (1.f + expf(-zv.x)), 1.f / (1.f + expf(-zv.y)));
+                }
+                const float2 ds = mul2(dh[i], s);
+                dzv[i] = mul2(ds, fma2(zv, add2(both(1.f), neg2(s)), both(1.f)));
+                dh[i] = mul2(ds, zv);
+            }
+        }
+        const uint32_t cut = ncut;
+        const float from_state = nin;
+        if (v0 > 0) fetch(v - stride, v0 + w * span - stride);
+
+        // the lane's maps of the state and of the adjoint
+        float A = 1.f, B = 0.f, M = 0.f;
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
             const bool c = kR && (cut >> i & 1u);
-            const float b = couple ? keep[i] * cx[i] : cx[i];
-            B = c ? b : fmaf(a[i], B, b);
-            A = c ? 0.f : A * a[i];
+            const float ai = i % 2 ? a[i / 2].y : a[i / 2].x, bi = i % 2 ? b[i / 2].y : b[i / 2].x;
+            B = c ? bi : fmaf(ai, B, bi);
+            A = c ? 0.f : A * ai;
         }
-        const uint32_t cuts = kR ? __ballot_sync(0xffffffffu, cut != 0) : 0u;
-        float M = 0.f, Am = A;
-        // dh, and the lane's map of the adjoint
-        float dh[kV], dzv[kV];
 #pragma unroll
         for (int i = kV - 1; i >= 0; --i) {
-            dh[i] = cd[i];
-            if constexpr (kZ) {
-                float s, c;
-                sigmoid2<kFast>(cz[i], s, c);
-                dzv[i] = dh[i] * (s * fmaf(cz[i], c, 1.f));
-                dh[i] *= cz[i] * s;
-            }
-            M = kR && (cut >> i & 1u) ? 0.f : a[i] * (dh[i] + M);
+            const float ai = i % 2 ? a[i / 2].y : a[i / 2].x, di = i % 2 ? dh[i / 2].y : dh[i / 2].x;
+            M = kR && (cut >> i & 1u) ? 0.f : ai * (di + M);
         }
-        scan_up<kR>(A, B, lane, cuts);
-        scan_down<kR>(Am, M, lane, cuts);
+        float Am = A;
+        const uint32_t cuts = kR ? __ballot_sync(0xffffffffu, cut != 0) : 0u;
+        scan_up<kR, kG>(A, B, lane, lanes, cuts);
+        scan_down<kR, kG>(Am, M, lane, lanes, cuts);
+        const int first = lane & ~(G - 1), last = lane | (G - 1);
+        const bool any = kR && (G == 32 ? cuts != 0 : (cuts & lanes_up_to(last, G == 32 ? 31 : G)) != 0);
         float Ax = __shfl_up_sync(0xffffffffu, A, 1), Bx = __shfl_up_sync(0xffffffffu, B, 1);
-        if (lane == 0) Ax = 1.f, Bx = 0.f;
-        const float Aw = __shfl_sync(0xffffffffu, Am, 0), Mw = __shfl_sync(0xffffffffu, M, 0);
+        if (in == 0) Ax = 1.f, Bx = 0.f;
+        const float Aw = __shfl_sync(0xffffffffu, Am, first), Mw = __shfl_sync(0xffffffffu, M, first);
         float Amx = __shfl_down_sync(0xffffffffu, Am, 1), Mx = __shfl_down_sync(0xffffffffu, M, 1);
-        if (lane == 31) Amx = 1.f, Mx = 0.f;
+        if (lane == last) Amx = 1.f, Mx = 0.f;
 
-        float from = carry;  // the adjoint reaching this warp's piece from behind
-        if constexpr (kMulti) {
-            carry = kR && cuts ? Mw : fmaf(Aw, carry, Mw);
-        } else {
-            if (lane == 0) pairs[buf][w] = {Aw, Mw, kR && cuts ? 1 : 0};
+        float from = carry;  // the adjoint reaching this warp's steps from behind
+        if constexpr (kShared) {
+            if (lane == 0) pairs[buf][w] = {Aw, Mw, any ? 1 : 0};
             __syncthreads();
             float c = carry;
             for (int k = W - 1; k >= 0; --k) {
@@ -298,32 +411,57 @@ __global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p) {
                 c = kR && q.cut ? q.B : fmaf(q.A, c, q.B);
             }
             carry = c;
+        } else {
+            carry = any ? Mw : fmaf(Aw, carry, Mw);
         }
-        float h = kR && (cuts & ((1u << lane) - 1u)) ? Bx : fmaf(Ax, in, Bx);
-        float before[kV];
+        // the states, from the one before the lane's steps
+        float h = kR && in > 0 && (cuts & lanes_up_to(lane - 1, in)) ? Bx : fmaf(Ax, from_state, Bx);
+        float2 before[kV / 2];
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const bool c = kR && (cut >> i & 1u);
-            const float b = couple ? keep[i] * cx[i] : cx[i];
-            before[i] = c ? 0.f : h;
-            h = c ? b : fmaf(a[i], h, b);
-            if constexpr (kZ) dzv[i] *= h;
+        for (int i = 0; i < kV / 2; ++i) {
+            float2 hv;
+            before[i].x = kR && (cut >> (2 * i) & 1u) ? 0.f : h;
+            hv.x = kR && (cut >> (2 * i) & 1u) ? b[i].x : fmaf(a[i].x, h, b[i].x);
+            before[i].y = kR && (cut >> (2 * i + 1) & 1u) ? 0.f : hv.x;
+            hv.y = kR && (cut >> (2 * i + 1) & 1u) ? b[i].y : fmaf(a[i].y, hv.x, b[i].y);
+            h = hv.y;
+            if constexpr (kZ) dzv[i] = mul2(dzv[i], hv);
         }
-        if constexpr (kZ) store8(static_cast<Tin *>(p.dz), base + v, lo, hi, vec, dzv);
-        const uint32_t behind = lane == 31 ? 0u : ~((2u << lane) - 1u);
-        float m = kR && (cuts & behind) ? Mx : fmaf(Amx, from, Mx);
+        // the adjoints, from the one behind them
+        const int after = last - lane;  // the row's lanes behind this one
+        float m = kR && after > 0 && (cuts & lanes_from(lane + 1, after)) ? Mx : fmaf(Amx, from, Mx);
+        float ox[kV], og[kV];
 #pragma unroll
-        for (int i = kV - 1; i >= 0; --i) {
-            const float lam = dh[i] + m;
-            const float da = lam * (couple ? before[i] - cx[i] : before[i]);
-            dh[i] = couple ? lam * keep[i] : lam;
-            before[i] = sigmoid ? da * (a[i] * keep[i]) : da;
-            m = kR && (cut >> i & 1u) ? 0.f : a[i] * lam;
+        for (int i = kV / 2 - 1; i >= 0; --i) {
+            float2 lam;
+            lam.y = dh[i].y + m;
+            m = kR && (cut >> (2 * i + 1) & 1u) ? 0.f : a[i].y * lam.y;
+            lam.x = dh[i].x + m;
+            m = kR && (cut >> (2 * i) & 1u) ? 0.f : a[i].x * lam.x;
+            float2 da = mul2(lam, couple ? add2(before[i], neg2(xv[i])) : before[i]);
+            if (sigmoid) da = mul2(da, mul2(a[i], keep[i]));
+            if (couple) lam = mul2(lam, keep[i]);
+            ox[2 * i] = lam.x, ox[2 * i + 1] = lam.y, og[2 * i] = da.x, og[2 * i + 1] = da.y;
         }
-        store8(static_cast<Tin *>(p.dx), base + v, lo, hi, vec, dh);
-        store8(static_cast<Tin *>(p.dg), base + v, lo, hi, vec, before);
+        if (!r.there) continue;
+        float oz[kV];
+        if constexpr (kZ) {
+#pragma unroll
+            for (int i = 0; i < kV / 2; ++i) oz[2 * i] = dzv[i].x, oz[2 * i + 1] = dzv[i].y;
+        }
+        if (inner && vec) {
+            store_vec(dx + v, ox);
+            store_vec(dg + v, og);
+            if constexpr (kZ) store_vec(dz + v, oz);
+        } else {
+            int lo, hi;
+            bounds_of(r, v, lo, hi);
+            store8(dx, v, lo, hi, vec, ox);
+            store8(dg, v, lo, hi, vec, og);
+            if constexpr (kZ) store8(dz, v, lo, hi, vec, oz);
+        }
     }
-    if (p.dh0 && lane == 0 && w == 0) p.dh0[row] = carry;
+    if (p.dh0 && r.there && in == 0 && w == 0) p.dh0[r.row] = carry;
 }
 
 // One step: a thread per row, the state read and written in place.
@@ -332,44 +470,56 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const GlrParams p) {
     constexpr bool kFast = sizeof(Tin) == 2;
     const int64_t row = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (row >= p.rows) return;
-    float a, keep;
-    gate<kFast>(load_elem(static_cast<const Tin *>(p.g), row), p.sigmoid, a, keep);
+    float2 a2, keep2;
+    gate2<kFast>(both(load_elem(static_cast<const Tin *>(p.g), row)), p.sigmoid, a2, keep2);
+    const float a = a2.x, keep = keep2.x;
     const float xv = load_elem(static_cast<const Tin *>(p.x), row);
     const float h = fmaf(a, p.last[row], p.couple ? keep * xv : xv);
     p.last[row] = h;
     float yv = h;
     if (p.z) {
-        const float zv = load_elem(static_cast<const Tin *>(p.z), row);
-        float s, c;
-        sigmoid2<kFast>(zv, s, c);
-        yv *= zv * s;
+        yv *= gated2<kFast>(both(load_elem(static_cast<const Tin *>(p.z), row))).x;
     }
     put(static_cast<Tout *>(p.y), row, yv);
 }
 
 int64_t pieces(int64_t L) { return (L + kV - 1 + kPiece - 1) / kPiece; }
 
-// Warps per row: as many as bring the GPU to about kWant warps per SM, no
-// more than the row has pieces.
-int glr_warps(int64_t rows, int64_t L) {
+// How rows are dealt out: `lanes` lanes each (a power of two) where a row is
+// short, else whole warps, as many as bring the GPU to about kWant warps per
+// SM, no more than the row feeds with `per_lane` steps a lane.
+struct GlrShape {
+    int lanes, warps;
+};
+GlrShape glr_shape(int64_t rows, int64_t L, int per_lane) {
     constexpr int kWant = 32;
-    const int64_t want = (int64_t)layer_sm_count() * kWant, n = pieces(L);
-    int w = 1;
-    while (w < kMaxWarps && rows * w < want && w < n) w *= 2;
-    return w;
+    const int64_t steps = L + kV - 1, want = (int64_t)layer_sm_count() * kWant;
+    GlrShape s{32, 1};
+    if (steps <= 16 * per_lane) {  // a row's steps in one turn
+        s.lanes = 4;
+        while (s.lanes * per_lane < steps) s.lanes *= 2;
+        return s;
+    }
+    while (s.warps < kMaxWarps && rows * s.warps < want && (int64_t)s.warps * 32 * per_lane < steps) s.warps *= 2;
+    return s;
 }
 
 template <typename Tin, typename Tout, bool kZ, bool kR>
 cudaError_t launch_glr(bool back, cudaStream_t s, const GlrParams &p) {
-    const int w = glr_warps(p.rows, p.L);
-    if (w == 1) {
-        constexpr int kRows = 4;
-        const unsigned grid = (unsigned)((p.rows + kRows - 1) / kRows);
-        if (back) glr_bwd_kernel<Tin, Tout, kZ, kR, true><<<grid, 32 * kRows, 0, s>>>(p);
-        else glr_fwd_kernel<Tin, Tout, kZ, kR, true><<<grid, 32 * kRows, 0, s>>>(p);
+    const GlrShape q = glr_shape(p.rows, p.L, back ? kV : 2 * kV);
+    constexpr int kThreads = 128;
+    const int64_t per = kThreads / q.lanes;
+    const unsigned grid = (unsigned)(q.warps > 1 ? p.rows : (p.rows + per - 1) / per);
+    const int threads = q.warps > 1 ? 32 * q.warps : kThreads;
+    if (q.lanes < 32) {
+        if (back) glr_bwd_kernel<Tin, Tout, kZ, kR, false, 0><<<grid, threads, 0, s>>>(p, q.lanes);
+        else glr_fwd_kernel<Tin, Tout, kZ, kR, false, 0><<<grid, threads, 0, s>>>(p, q.lanes);
+    } else if (q.warps == 1) {
+        if (back) glr_bwd_kernel<Tin, Tout, kZ, kR, false, 32><<<grid, threads, 0, s>>>(p, 32);
+        else glr_fwd_kernel<Tin, Tout, kZ, kR, false, 32><<<grid, threads, 0, s>>>(p, 32);
     } else {
-        if (back) glr_bwd_kernel<Tin, Tout, kZ, kR, false><<<(unsigned)p.rows, 32 * w, 0, s>>>(p);
-        else glr_fwd_kernel<Tin, Tout, kZ, kR, false><<<(unsigned)p.rows, 32 * w, 0, s>>>(p);
+        if (back) glr_bwd_kernel<Tin, Tout, kZ, kR, true, 32><<<grid, threads, 0, s>>>(p, 32);
+        else glr_fwd_kernel<Tin, Tout, kZ, kR, true, 32><<<grid, threads, 0, s>>>(p, 32);
     }
     return cudaGetLastError();
 }

@@ -11,8 +11,9 @@ autograd Functions.  Sequences are (batch, dim, L) as everywhere in this
 library; the norm also takes (rows, dim).
 
 All tensors of a call lie on one CUDA device, which need not be the current
-one.  Work is queued on that device's current stream, or on ``stream``; copies
-of non-contiguous inputs are made on the same stream.  Outputs must be
+one.  Work is queued on that device's current stream, or on the ``stream`` that
+every call but the ``_fn`` forms takes by keyword; copies of non-contiguous
+inputs are made on the same stream.  Outputs must be
 contiguous.  A wrong shape, dtype or device raises ValueError, a call that the
 library rejects SelscanError.
 
@@ -23,8 +24,8 @@ requires it: warm up on a side stream, and keep no eager graph of the same
 leaves alive while a backward pass is captured (torch ends the process when a
 captured backward meets a leaf's accumulation on another stream).
 """
-import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -39,46 +40,59 @@ __all__ = ["ss_norm_fwd", "ss_norm_bwd", "ss_norm_bwd_workspace_bytes", "layer_n
 _F32 = torch.float32
 
 
-def _where(x, stream):
-    """The context a call is made in: x's device, and ``stream`` when given."""
-    if stream is not None:
+def _on_device(fn):
+    """Runs ``fn(x, ...)`` on ``stream`` when given, and otherwise on the
+    current stream of x's device, whichever device is current."""
+    @functools.wraps(fn)
+    def call(x, *args, stream=None, **kw):
+        if stream is None:
+            if not x.is_cuda or x.get_device() == torch._C._cuda_getDevice():
+                return fn(x, *args, **kw)
+            with torch.cuda.device(x.device):
+                return fn(x, *args, **kw)
         if stream.device != x.device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {x.device}")
-        return torch.cuda.stream(stream)  # also sets the device
-    if x.is_cuda and x.device.index != torch.cuda.current_device():
-        return torch.cuda.device(x.device)
-    return contextlib.nullcontext()
+        with torch.cuda.stream(stream):  # also sets the device
+            return fn(x, *args, **kw)
+    return call
 
 
 def _stream(x):
     if not x.is_cuda:
         raise ValueError(f"the library runs on CUDA tensors only, got one on {x.device}")
-    return torch._C._cuda_getCurrentRawStream(x.device.index)
+    return torch._C._cuda_getCurrentRawStream(x.get_device())
 
 
-def _input(t, name, shape, dtype, device):
-    """``t`` (or None) as a dense tensor of that shape, dtype and device."""
+def _refuse(t, name, shape, dtype, x):
+    raise ValueError(f"{name} must be a {tuple(shape)} {dtype} tensor on {x.device}, got {tuple(t.shape)} {t.dtype} "
+                     f"on {t.device}")
+
+
+def _input(t, name, shape, dtype, x):
+    """``t`` (or None) as a dense tensor of that shape and dtype on x's device."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype is not dtype or t.device != device:
-        raise ValueError(f"{name} must be a {tuple(shape)} {dtype} tensor on {device}, got {tuple(t.shape)} "
-                         f"{t.dtype} on {t.device}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != x.get_device():
+        _refuse(t, name, shape, dtype, x)
     return t if t.is_contiguous() else t.contiguous()
 
 
-def _output(t, name, shape, dtype, device):
+def _output(t, name, shape, dtype, x):
     """``t`` (or None) checked as an output, which is never copied."""
-    if t is not None and (t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on {device}")
+    if t is not None:
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != x.get_device():
+            _refuse(t, name, shape, dtype, x)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
     return t
 
 
-def _starts(reset, batch, L, device):
+def _starts(reset, batch, L, x):
     if reset is None:
         return None
     if reset.dtype is torch.bool:
         reset = reset.view(torch.uint8)
-    return _input(reset, "reset", (batch, L), torch.uint8, device)
+    return _input(reset, "reset", (batch, L), torch.uint8, x)
 
 
 def _main(x, dims, what):
@@ -97,8 +111,21 @@ def _out_type(dtype, x, name):
     return dtype
 
 
+def _new(x, dtype=None):
+    """A dense tensor of x's shape."""
+    if (dtype is None or dtype is x.dtype) and x.is_contiguous():
+        return torch.empty_like(x)
+    return torch.empty(x.shape, dtype=dtype or x.dtype, device=x.device)
+
+
+@functools.lru_cache(maxsize=1024)
+def _sizes(batch, dim, L, in_dtype, out_dtype):
+    """The descriptor of these sizes, by reference (made once for each)."""
+    return ctypes.byref(Desc(batch, dim, L, 0, _DTYPE_CODE[in_dtype], _DTYPE_CODE[out_dtype]))
+
+
 def _desc(batch, dim, L, x, out_dtype):
-    return ctypes.byref(Desc(batch, dim, L, 0, _DTYPE_CODE[x.dtype], _DTYPE_CODE[out_dtype]))
+    return _sizes(batch, dim, L, x.dtype, out_dtype)
 
 
 def _p(t):
@@ -112,31 +139,36 @@ def _norm_sizes(x):
     return (x.shape[0], x.shape[1], 1 if x.dim() == 2 else x.shape[2])
 
 
-def ss_norm_fwd(x, y, weight=None, bias=None, eps=1e-5, rms=False, mean=None, rstd=None, stream=None):
+def _norm_fwd(x, y, weight, bias, eps, rms, mean, rstd):
+    batch, dim, L = _norm_sizes(x)
+    weight, bias = _input(weight, "weight", (dim,), _F32, x), _input(bias, "bias", (dim,), _F32, x)
+    _check(lib().ss_norm_fwd(_desc(batch, dim, L, x, y.dtype), x.data_ptr(), _p(weight), _p(bias), eps,
+                             1 if rms else 0, y.data_ptr(), _p(mean), _p(rstd), _stream(x)), "ss_norm_fwd")
+
+
+@_on_device
+def ss_norm_fwd(x, y, weight=None, bias=None, eps=1e-5, rms=False, mean=None, rstd=None):
     """Queue the normalisation of x ((batch, dim, L), or (rows, dim)) over its
     channels into y.  weight, bias: (dim,) float32; mean, rstd: float32
     outputs of x's shape without its channels (mean only without ``rms``)."""
-    with _where(x, stream):
-        x = _main(x, (2, 3), "x")
-        batch, dim, L = _norm_sizes(x)
-        dev, kept = x.device, x.shape[:1] + x.shape[2:]
-        _output(y, "y", x.shape, _out_type(y.dtype, x, "y"), dev)
-        weight, bias = _input(weight, "weight", (dim,), _F32, dev), _input(bias, "bias", (dim,), _F32, dev)
-        _output(mean, "mean", kept, _F32, dev), _output(rstd, "rstd", kept, _F32, dev)
-        _check(lib().ss_norm_fwd(_desc(batch, dim, L, x, y.dtype), x.data_ptr(), _p(weight), _p(bias), eps,
-                                 1 if rms else 0, y.data_ptr(), _p(mean), _p(rstd), _stream(x)), "ss_norm_fwd")
+    x = _main(x, (2, 3), "x")
+    kept = x.shape[:1] + x.shape[2:]
+    _output(y, "y", x.shape, _out_type(y.dtype, x, "y"), x)
+    _output(mean, "mean", kept, _F32, x), _output(rstd, "rstd", kept, _F32, x)
+    _norm_fwd(x, y, weight, bias, eps, rms, mean, rstd)
 
 
-def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, rms=False, return_stats=False, out_dtype=None, stream=None):
+@_on_device
+def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, rms=False, return_stats=False, out_dtype=None):
     """y, or (y, mean, rstd) with ``return_stats`` (mean is None with ``rms``)."""
-    with _where(x, stream):
-        y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-        mean = rstd = None
-        if return_stats:
-            kept = x.shape[:1] + x.shape[2:]
-            rstd = torch.empty(kept, dtype=_F32, device=x.device)
-            mean = None if rms else torch.empty(kept, dtype=_F32, device=x.device)
-        ss_norm_fwd(x, y, weight, bias, eps, rms, mean, rstd)
+    x = _main(x, (2, 3), "x")
+    y = _new(x, out_dtype and _out_type(out_dtype, x, "out_dtype"))
+    mean = rstd = None
+    if return_stats:
+        kept = x.shape[:1] + x.shape[2:]
+        rstd = torch.empty(kept, dtype=_F32, device=x.device)
+        mean = None if rms else torch.empty(kept, dtype=_F32, device=x.device)
+    _norm_fwd(x, y, weight, bias, eps, rms, mean, rstd)
     return (y, mean, rstd) if return_stats else y
 
 
@@ -145,42 +177,42 @@ def ss_norm_bwd_workspace_bytes(batch, dim, seqlen, in_dtype=torch.bfloat16, out
     return int(lib().ss_norm_bwd_workspace_bytes(ctypes.byref(desc)))
 
 
-def ss_norm_bwd(x, dy, rstd, dx, mean=None, weight=None, dweight=None, dbias=None, workspace=None, stream=None):
+@_on_device
+def ss_norm_bwd(x, dy, rstd, dx, mean=None, weight=None, dweight=None, dbias=None, workspace=None):
     """Queue the norm's backward from the forward's mean and rstd (mean None:
     the RMS form) into dx and, where given, dweight and dbias ((dim,) float32).
     ``workspace``: a CUDA tensor of ss_norm_bwd_workspace_bytes() bytes, made
     here when None and needed."""
-    with _where(x, stream):
-        x = _main(x, (2, 3), "x")
-        batch, dim, L = _norm_sizes(x)
-        dev, kept = x.device, x.shape[:1] + x.shape[2:]
-        dy = _input(dy, "dy", x.shape, _out_type(dy.dtype, x, "dy"), dev)
-        mean, rstd = _input(mean, "mean", kept, _F32, dev), _input(rstd, "rstd", kept, _F32, dev)
-        weight = _input(weight, "weight", (dim,), _F32, dev)
-        _output(dx, "dx", x.shape, x.dtype, dev)
-        _output(dweight, "dweight", (dim,), _F32, dev), _output(dbias, "dbias", (dim,), _F32, dev)
-        desc = _desc(batch, dim, L, x, dy.dtype)
-        if workspace is None and (dweight is not None or dbias is not None):
-            n = lib().ss_norm_bwd_workspace_bytes(desc)
-            workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
-        size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(lib().ss_norm_bwd(desc, x.data_ptr(), _p(weight), _p(mean), rstd.data_ptr(), dy.data_ptr(),
-                                 dx.data_ptr(), _p(dweight), _p(dbias), _p(workspace), size, _stream(x)),
-               "ss_norm_bwd")
+    x = _main(x, (2, 3), "x")
+    batch, dim, L = _norm_sizes(x)
+    kept = x.shape[:1] + x.shape[2:]
+    dy = _input(dy, "dy", x.shape, _out_type(dy.dtype, x, "dy"), x)
+    mean, rstd = _input(mean, "mean", kept, _F32, x), _input(rstd, "rstd", kept, _F32, x)
+    weight = _input(weight, "weight", (dim,), _F32, x)
+    _output(dx, "dx", x.shape, x.dtype, x)
+    _output(dweight, "dweight", (dim,), _F32, x), _output(dbias, "dbias", (dim,), _F32, x)
+    desc = _desc(batch, dim, L, x, dy.dtype)
+    if workspace is None and (dweight is not None or dbias is not None):
+        n = lib().ss_norm_bwd_workspace_bytes(desc)
+        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().ss_norm_bwd(desc, x.data_ptr(), _p(weight), _p(mean), rstd.data_ptr(), dy.data_ptr(),
+                             dx.data_ptr(), _p(dweight), _p(dbias), _p(workspace), size, _stream(x)),
+           "ss_norm_bwd")
 
 
-def layer_norm_bwd(x, dy, rstd, mean=None, weight=None, bias=None, rms=False, stream=None):
+@_on_device
+def layer_norm_bwd(x, dy, rstd, mean=None, weight=None, bias=None, rms=False):
     """Gradients of sum(dy * y) as a dict: dx, dweight (None without weight),
     dbias (None without bias).  mean and rstd are layer_norm_fwd's
     (``return_stats``); ``rms`` as there."""
     if (mean is None) != bool(rms):
         raise ValueError("mean goes with the layer norm, none with rms")
-    with _where(x, stream):
-        dim, dev = x.shape[1], x.device
-        g = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev),
-             "dweight": torch.empty(dim, dtype=_F32, device=dev) if weight is not None else None,
-             "dbias": torch.empty(dim, dtype=_F32, device=dev) if bias is not None else None}
-        ss_norm_bwd(x, dy, rstd, g["dx"], mean, weight, g["dweight"], g["dbias"])
+    dim, dev = x.shape[1], x.device
+    g = {"dx": _new(x),
+         "dweight": torch.empty(dim, dtype=_F32, device=dev) if weight is not None else None,
+         "dbias": torch.empty(dim, dtype=_F32, device=dev) if bias is not None else None}
+    ss_norm_bwd(x, dy, rstd, g["dx"], mean, weight, g["dweight"], g["dbias"])
     return g
 
 
@@ -213,96 +245,106 @@ def layer_norm_fn(x, weight=None, bias=None, eps=1e-5, rms=False):
 # -------------------------------------------------------- the causal convolution
 
 
-def _conv_sizes(x, weight):
-    if weight.dim() != 2:
-        raise ValueError("weight must be (dim, width)")
+def _width(weight):
+    if weight.dim() != 2 or not 2 <= weight.shape[1] <= 8:
+        raise ValueError(f"weight must be (dim, width) with a width from 2 to 8, got {tuple(weight.shape)}")
     return weight.shape[1]
 
 
-def ss_conv_fwd(x, weight, y, bias=None, silu=False, initial_state=None, reset=None, last_state=None, stream=None):
+def _conv_fwd(x, weight, y, bias, silu, initial_state, reset, last_state):
+    (batch, dim, L), W = x.shape, _width(weight)
+    weight, bias = _input(weight, "weight", (dim, W), _F32, x), _input(bias, "bias", (dim,), _F32, x)
+    initial_state = _input(initial_state, "initial_state", (batch, dim, W - 1), x.dtype, x)
+    reset = _starts(reset, batch, L, x)
+    _check(lib().ss_conv_fwd(_desc(batch, dim, L, x, y.dtype), W, x.data_ptr(), weight.data_ptr(), _p(bias),
+                             1 if silu else 0, _p(initial_state), _p(reset), y.data_ptr(), _p(last_state),
+                             _stream(x)), "ss_conv_fwd")
+
+
+@_on_device
+def ss_conv_fwd(x, weight, y, bias=None, silu=False, initial_state=None, reset=None, last_state=None):
     """Queue the causal depthwise convolution of x (batch, dim, L) into y.
     weight: (dim, width) float32, width 2..8; bias: (dim,) float32;
     initial_state, last_state: (batch, dim, width - 1) in x's dtype, two
     buffers; reset: (batch, L) uint8 or bool, nonzero where a sequence starts."""
-    with _where(x, stream):
-        x = _main(x, (3,), "x")
-        (batch, dim, L), W, dev = x.shape, _conv_sizes(x, weight), x.device
-        state = (batch, dim, W - 1)
-        weight, bias = _input(weight, "weight", (dim, W), _F32, dev), _input(bias, "bias", (dim,), _F32, dev)
-        initial_state, reset = _input(initial_state, "initial_state", state, x.dtype, dev), _starts(reset, batch, L, dev)
-        _output(y, "y", x.shape, _out_type(y.dtype, x, "y"), dev), _output(last_state, "last_state", state, x.dtype, dev)
-        _check(lib().ss_conv_fwd(_desc(batch, dim, L, x, y.dtype), W, x.data_ptr(), weight.data_ptr(), _p(bias),
-                                 1 if silu else 0, _p(initial_state), _p(reset), y.data_ptr(), _p(last_state),
-                                 _stream(x)), "ss_conv_fwd")
+    x = _main(x, (3,), "x")
+    _output(y, "y", x.shape, _out_type(y.dtype, x, "y"), x)
+    _output(last_state, "last_state", (*x.shape[:2], _width(weight) - 1), x.dtype, x)
+    _conv_fwd(x, weight, y, bias, silu, initial_state, reset, last_state)
 
 
+@_on_device
 def causal_conv_fwd(x, weight, bias=None, silu=False, initial_state=None, reset=None, return_last_state=False,
-                    out_dtype=None, stream=None):
+                    out_dtype=None):
     """y (and the last state) of the causal depthwise convolution."""
-    with _where(x, stream):
-        y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-        last = None
-        if return_last_state:
-            last = torch.empty((*x.shape[:2], max(_conv_sizes(x, weight) - 1, 0)), dtype=x.dtype, device=x.device)
-        ss_conv_fwd(x, weight, y, bias, silu, initial_state, reset, last)
+    x = _main(x, (3,), "x")
+    y = _new(x, out_dtype and _out_type(out_dtype, x, "out_dtype"))
+    last = None
+    if return_last_state:
+        last = torch.empty((*x.shape[:2], _width(weight) - 1), dtype=x.dtype, device=x.device)
+    _conv_fwd(x, weight, y, bias, silu, initial_state, reset, last)
     return (y, last) if return_last_state else y
 
 
+@_on_device
 def ss_conv_bwd(x, weight, dy, dx, bias=None, silu=False, initial_state=None, reset=None, d_last_state=None,
-                dweight=None, dbias=None, dinitial_state=None, stream=None):
+                dweight=None, dbias=None, dinitial_state=None):
     """Queue the convolution's backward into dx and, where given, dweight
     ((dim, width) float32), dbias ((dim,) float32) and dinitial_state."""
-    with _where(x, stream):
-        x = _main(x, (3,), "x")
-        (batch, dim, L), W, dev = x.shape, _conv_sizes(x, weight), x.device
-        state = (batch, dim, W - 1)
-        weight, bias = _input(weight, "weight", (dim, W), _F32, dev), _input(bias, "bias", (dim,), _F32, dev)
-        initial_state, reset = _input(initial_state, "initial_state", state, x.dtype, dev), _starts(reset, batch, L, dev)
-        dy = _input(dy, "dy", x.shape, _out_type(dy.dtype, x, "dy"), dev)
-        d_last_state = _input(d_last_state, "d_last_state", state, x.dtype, dev)
-        _output(dx, "dx", x.shape, x.dtype, dev), _output(dinitial_state, "dinitial_state", state, x.dtype, dev)
-        _output(dweight, "dweight", (dim, W), _F32, dev), _output(dbias, "dbias", (dim,), _F32, dev)
-        _check(lib().ss_conv_bwd(_desc(batch, dim, L, x, dy.dtype), W, x.data_ptr(), weight.data_ptr(), _p(bias),
-                                 1 if silu else 0, _p(initial_state), _p(reset), dy.data_ptr(), _p(d_last_state),
-                                 dx.data_ptr(), _p(dweight), _p(dbias), _p(dinitial_state), _stream(x)),
-               "ss_conv_bwd")
+    x = _main(x, (3,), "x")
+    (batch, dim, L), W = x.shape, _width(weight)
+    state = (batch, dim, W - 1)
+    weight, bias = _input(weight, "weight", (dim, W), _F32, x), _input(bias, "bias", (dim,), _F32, x)
+    initial_state, reset = _input(initial_state, "initial_state", state, x.dtype, x), _starts(reset, batch, L, x)
+    dy = _input(dy, "dy", x.shape, _out_type(dy.dtype, x, "dy"), x)
+    d_last_state = _input(d_last_state, "d_last_state", state, x.dtype, x)
+    _output(dx, "dx", x.shape, x.dtype, x), _output(dinitial_state, "dinitial_state", state, x.dtype, x)
+    _output(dweight, "dweight", (dim, W), _F32, x), _output(dbias, "dbias", (dim,), _F32, x)
+    _check(lib().ss_conv_bwd(_desc(batch, dim, L, x, dy.dtype), W, x.data_ptr(), weight.data_ptr(), _p(bias),
+                             1 if silu else 0, _p(initial_state), _p(reset), dy.data_ptr(), _p(d_last_state),
+                             dx.data_ptr(), _p(dweight), _p(dbias), _p(dinitial_state), _stream(x)),
+           "ss_conv_bwd")
 
 
-def causal_conv_bwd(x, weight, dy, bias=None, silu=False, initial_state=None, reset=None, d_last_state=None,
-                    stream=None):
+@_on_device
+def causal_conv_bwd(x, weight, dy, bias=None, silu=False, initial_state=None, reset=None, d_last_state=None):
     """Gradients of sum(dy * y) (+ sum(d_last_state * last state)) as a dict:
     dx, dweight, dbias (None without bias), dinitial_state (None without an
     initial state)."""
-    with _where(x, stream):
-        dev = x.device
-        g = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev),
-             "dweight": torch.empty(weight.shape, dtype=_F32, device=dev),
-             "dbias": torch.empty(x.shape[1], dtype=_F32, device=dev) if bias is not None else None,
-             "dinitial_state": torch.empty(initial_state.shape, dtype=x.dtype, device=dev)
-             if initial_state is not None else None}
-        ss_conv_bwd(x, weight, dy, g["dx"], bias, silu, initial_state, reset, d_last_state, g["dweight"],
-                    g["dbias"], g["dinitial_state"])
+    dev = x.device
+    g = {"dx": _new(x),
+         "dweight": torch.empty(weight.shape, dtype=_F32, device=dev),
+         "dbias": torch.empty(x.shape[1], dtype=_F32, device=dev) if bias is not None else None,
+         "dinitial_state": torch.empty(initial_state.shape, dtype=x.dtype, device=dev)
+         if initial_state is not None else None}
+    ss_conv_bwd(x, weight, dy, g["dx"], bias, silu, initial_state, reset, d_last_state, g["dweight"],
+                g["dbias"], g["dinitial_state"])
     return g
 
 
-def ss_conv_step(x, weight, state, y, bias=None, silu=False, stream=None):
+def _conv_step(x, weight, state, y, bias, silu):
+    (batch, dim), W = x.shape, _width(weight)
+    weight, bias = _input(weight, "weight", (dim, W), _F32, x), _input(bias, "bias", (dim,), _F32, x)
+    _output(state, "state", (batch, dim, W - 1), x.dtype, x)
+    _check(lib().ss_conv_step(_desc(batch, dim, 1, x, y.dtype), W, x.data_ptr(), weight.data_ptr(), _p(bias),
+                              1 if silu else 0, state.data_ptr(), y.data_ptr(), _stream(x)), "ss_conv_step")
+
+
+@_on_device
+def ss_conv_step(x, weight, state, y, bias=None, silu=False):
     """Queue one decoding step: x, y (batch, dim); state (batch, dim, width -
     1) in x's dtype, updated in place."""
-    with _where(x, stream):
-        x = _main(x, (2,), "x")
-        (batch, dim), W, dev = x.shape, _conv_sizes(x, weight), x.device
-        weight, bias = _input(weight, "weight", (dim, W), _F32, dev), _input(bias, "bias", (dim,), _F32, dev)
-        _output(state, "state", (batch, dim, W - 1), x.dtype, dev)
-        _output(y, "y", x.shape, _out_type(y.dtype, x, "y"), dev)
-        _check(lib().ss_conv_step(_desc(batch, dim, 1, x, y.dtype), W, x.data_ptr(), weight.data_ptr(), _p(bias),
-                                  1 if silu else 0, state.data_ptr(), y.data_ptr(), _stream(x)), "ss_conv_step")
+    x = _main(x, (2,), "x")
+    _output(y, "y", x.shape, _out_type(y.dtype, x, "y"), x)
+    _conv_step(x, weight, state, y, bias, silu)
 
 
-def causal_conv_step(x, weight, state, bias=None, silu=False, out_dtype=None, stream=None):
+@_on_device
+def causal_conv_step(x, weight, state, bias=None, silu=False, out_dtype=None):
     """y (batch, dim) of one decoding step; the state is updated in place."""
-    with _where(x, stream):
-        y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-        ss_conv_step(x, weight, state, y, bias, silu)
+    x = _main(x, (2,), "x")
+    y = _new(x, out_dtype and _out_type(out_dtype, x, "out_dtype"))
+    _conv_step(x, weight, state, y, bias, silu)
     return y
 
 
@@ -340,98 +382,104 @@ def ss_glr_ckpt_elems(batch, dim, seqlen, in_dtype=torch.bfloat16, out_dtype=Non
     return int(lib().ss_glr_ckpt_elems(ctypes.byref(desc)))
 
 
+@_on_device
 def ss_glr_fwd(x, g, y, z=None, gate_sigmoid=True, couple=False, initial_state=None, reset=None, last_state=None,
-               ckpt=None, stream=None):
+               ckpt=None):
     """Queue the gated linear recurrence of x, g (batch, dim, L) into y (None:
     only the states are wanted).  z: output gate; initial_state, last_state:
     (batch, dim) float32, one buffer or two; reset: (batch, L) uint8 or bool,
     nonzero where a sequence starts; ckpt: ss_glr_ckpt_elems() float32, for
     the backward."""
-    with _where(x, stream):
-        x = _main(x, (3,), "x")
-        (batch, dim, L), dev = x.shape, x.device
-        g, z = _input(g, "g", x.shape, x.dtype, dev), _input(z, "z", x.shape, x.dtype, dev)
-        out = x.dtype if y is None else _out_type(y.dtype, x, "y")
-        _output(y, "y", x.shape, out, dev), _output(last_state, "last_state", (batch, dim), _F32, dev)
-        initial_state = _input(initial_state, "initial_state", (batch, dim), _F32, dev)
-        reset, desc = _starts(reset, batch, L, dev), _desc(batch, dim, L, x, out)
-        if ckpt is not None:
-            _output(ckpt, "ckpt", (int(lib().ss_glr_ckpt_elems(desc)),), _F32, dev)
-        _check(lib().ss_glr_fwd(desc, x.data_ptr(), g.data_ptr(), _p(z), 1 if gate_sigmoid else 0,
-                                1 if couple else 0, _p(initial_state), _p(reset), _p(y), _p(last_state), _p(ckpt),
-                                _stream(x)), "ss_glr_fwd")
+    x = _main(x, (3,), "x")
+    batch, dim, L = x.shape
+    g, z = _input(g, "g", x.shape, x.dtype, x), _input(z, "z", x.shape, x.dtype, x)
+    out = x.dtype if y is None else _out_type(y.dtype, x, "y")
+    _output(y, "y", x.shape, out, x), _output(last_state, "last_state", (batch, dim), _F32, x)
+    initial_state = _input(initial_state, "initial_state", (batch, dim), _F32, x)
+    reset, desc = _starts(reset, batch, L, x), _desc(batch, dim, L, x, out)
+    if ckpt is not None:
+        _output(ckpt, "ckpt", (int(lib().ss_glr_ckpt_elems(desc)),), _F32, x)
+    _check(lib().ss_glr_fwd(desc, x.data_ptr(), g.data_ptr(), _p(z), 1 if gate_sigmoid else 0,
+                            1 if couple else 0, _p(initial_state), _p(reset), _p(y), _p(last_state), _p(ckpt),
+                            _stream(x)), "ss_glr_fwd")
 
 
+@_on_device
 def gated_recurrence_fwd(x, g, z=None, gate_sigmoid=True, couple=False, initial_state=None, reset=None,
-                         return_last_state=False, return_ckpt=False, out_dtype=None, stream=None):
+                         return_last_state=False, return_ckpt=False, out_dtype=None):
     """y of the gated linear recurrence, then the last state
     (``return_last_state``) and the backward's checkpoints (``return_ckpt``)."""
-    with _where(x, stream):
-        out = out_dtype or x.dtype
-        y = torch.empty(x.shape, dtype=out, device=x.device)
-        last = torch.empty(x.shape[:2], dtype=_F32, device=x.device) if return_last_state else None
-        ckpt = None
-        if return_ckpt:
-            n = lib().ss_glr_ckpt_elems(_desc(*x.shape, x, _out_type(out, x, "out_dtype")))
-            ckpt = torch.empty(n, dtype=_F32, device=x.device)
-        ss_glr_fwd(x, g, y, z, gate_sigmoid, couple, initial_state, reset, last, ckpt)
+    out = out_dtype or x.dtype
+    y = _new(x, out)
+    last = torch.empty(x.shape[:2], dtype=_F32, device=x.device) if return_last_state else None
+    ckpt = None
+    if return_ckpt:
+        n = lib().ss_glr_ckpt_elems(_desc(*x.shape, x, _out_type(out, x, "out_dtype")))
+        ckpt = torch.empty(n, dtype=_F32, device=x.device)
+    ss_glr_fwd(x, g, y, z, gate_sigmoid, couple, initial_state, reset, last, ckpt)
     more = ((last,) if return_last_state else ()) + ((ckpt,) if return_ckpt else ())
     return (y, *more) if more else y
 
 
+@_on_device
 def ss_glr_bwd(x, g, dy, ckpt, dx, dg, z=None, dz=None, gate_sigmoid=True, couple=False, reset=None,
-               d_last_state=None, dinitial_state=None, stream=None):
+               d_last_state=None, dinitial_state=None):
     """Queue the recurrence's backward, from the forward's checkpoints, into
     dx, dg, dz (with z) and, where given, dinitial_state."""
-    with _where(x, stream):
-        x = _main(x, (3,), "x")
-        (batch, dim, L), dev = x.shape, x.device
-        g, z = _input(g, "g", x.shape, x.dtype, dev), _input(z, "z", x.shape, x.dtype, dev)
-        dy = _input(dy, "dy", x.shape, _out_type(dy.dtype, x, "dy"), dev)
-        desc, reset = _desc(batch, dim, L, x, dy.dtype), _starts(reset, batch, L, dev)
-        ckpt = _input(ckpt, "ckpt", (int(lib().ss_glr_ckpt_elems(desc)),), _F32, dev)
-        d_last_state = _input(d_last_state, "d_last_state", (batch, dim), _F32, dev)
-        _output(dx, "dx", x.shape, x.dtype, dev), _output(dg, "dg", x.shape, x.dtype, dev)
-        _output(dz, "dz", x.shape, x.dtype, dev), _output(dinitial_state, "dinitial_state", (batch, dim), _F32, dev)
-        _check(lib().ss_glr_bwd(desc, x.data_ptr(), g.data_ptr(), _p(z), 1 if gate_sigmoid else 0,
-                                1 if couple else 0, _p(reset), ckpt.data_ptr(), dy.data_ptr(), _p(d_last_state),
-                                dx.data_ptr(), dg.data_ptr(), _p(dz), _p(dinitial_state), _stream(x)), "ss_glr_bwd")
+    x = _main(x, (3,), "x")
+    batch, dim, L = x.shape
+    g, z = _input(g, "g", x.shape, x.dtype, x), _input(z, "z", x.shape, x.dtype, x)
+    dy = _input(dy, "dy", x.shape, _out_type(dy.dtype, x, "dy"), x)
+    desc, reset = _desc(batch, dim, L, x, dy.dtype), _starts(reset, batch, L, x)
+    ckpt = _input(ckpt, "ckpt", (int(lib().ss_glr_ckpt_elems(desc)),), _F32, x)
+    d_last_state = _input(d_last_state, "d_last_state", (batch, dim), _F32, x)
+    _output(dx, "dx", x.shape, x.dtype, x), _output(dg, "dg", x.shape, x.dtype, x)
+    _output(dz, "dz", x.shape, x.dtype, x), _output(dinitial_state, "dinitial_state", (batch, dim), _F32, x)
+    _check(lib().ss_glr_bwd(desc, x.data_ptr(), g.data_ptr(), _p(z), 1 if gate_sigmoid else 0,
+                            1 if couple else 0, _p(reset), ckpt.data_ptr(), dy.data_ptr(), _p(d_last_state),
+                            dx.data_ptr(), dg.data_ptr(), _p(dz), _p(dinitial_state), _stream(x)), "ss_glr_bwd")
 
 
+@_on_device
 def gated_recurrence_bwd(x, g, dy, ckpt, z=None, gate_sigmoid=True, couple=False, reset=None, d_last_state=None,
-                         return_dinitial_state=False, stream=None):
+                         return_dinitial_state=False):
     """Gradients of sum(dy * y) (+ sum(d_last_state * last state)) as a dict:
     dx, dg, dz (None without z), dinitial_state (None unless asked for).
     ckpt: gated_recurrence_fwd's, of the same inputs, initial state and starts."""
-    with _where(x, stream):
-        dev = x.device
-        d = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev),
-             "dg": torch.empty(x.shape, dtype=x.dtype, device=dev),
-             "dz": torch.empty(x.shape, dtype=x.dtype, device=dev) if z is not None else None,
-             "dinitial_state": torch.empty(x.shape[:2], dtype=_F32, device=dev) if return_dinitial_state else None}
-        ss_glr_bwd(x, g, dy, ckpt, d["dx"], d["dg"], z, d["dz"], gate_sigmoid, couple, reset, d_last_state,
-                   d["dinitial_state"])
+    dev = x.device
+    d = {"dx": _new(x),
+         "dg": _new(x),
+         "dz": _new(x) if z is not None else None,
+         "dinitial_state": torch.empty(x.shape[:2], dtype=_F32, device=dev) if return_dinitial_state else None}
+    ss_glr_bwd(x, g, dy, ckpt, d["dx"], d["dg"], z, d["dz"], gate_sigmoid, couple, reset, d_last_state,
+               d["dinitial_state"])
     return d
 
 
-def ss_glr_step(x, g, state, y, z=None, gate_sigmoid=True, couple=False, stream=None):
+def _glr_step(x, g, state, y, z, gate_sigmoid, couple):
+    batch, dim = x.shape
+    g, z = _input(g, "g", x.shape, x.dtype, x), _input(z, "z", x.shape, x.dtype, x)
+    _output(state, "state", x.shape, _F32, x)
+    _check(lib().ss_glr_step(_desc(batch, dim, 1, x, y.dtype), x.data_ptr(), g.data_ptr(), _p(z),
+                             1 if gate_sigmoid else 0, 1 if couple else 0, state.data_ptr(), y.data_ptr(),
+                             _stream(x)), "ss_glr_step")
+
+
+@_on_device
+def ss_glr_step(x, g, state, y, z=None, gate_sigmoid=True, couple=False):
     """Queue one decoding step: x, g, z, y (batch, dim); state (batch, dim)
     float32, updated in place."""
-    with _where(x, stream):
-        x = _main(x, (2,), "x")
-        (batch, dim), dev = x.shape, x.device
-        g, z = _input(g, "g", x.shape, x.dtype, dev), _input(z, "z", x.shape, x.dtype, dev)
-        _output(state, "state", x.shape, _F32, dev), _output(y, "y", x.shape, _out_type(y.dtype, x, "y"), dev)
-        _check(lib().ss_glr_step(_desc(batch, dim, 1, x, y.dtype), x.data_ptr(), g.data_ptr(), _p(z),
-                                 1 if gate_sigmoid else 0, 1 if couple else 0, state.data_ptr(), y.data_ptr(),
-                                 _stream(x)), "ss_glr_step")
+    x = _main(x, (2,), "x")
+    _output(y, "y", x.shape, _out_type(y.dtype, x, "y"), x)
+    _glr_step(x, g, state, y, z, gate_sigmoid, couple)
 
 
-def gated_recurrence_step(x, g, state, z=None, gate_sigmoid=True, couple=False, out_dtype=None, stream=None):
+@_on_device
+def gated_recurrence_step(x, g, state, z=None, gate_sigmoid=True, couple=False, out_dtype=None):
     """y (batch, dim) of one decoding step; the state is updated in place."""
-    with _where(x, stream):
-        y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-        ss_glr_step(x, g, state, y, z, gate_sigmoid, couple)
+    x = _main(x, (2,), "x")
+    y = _new(x, out_dtype and _out_type(out_dtype, x, "out_dtype"))
+    _glr_step(x, g, state, y, z, gate_sigmoid, couple)
     return y
 
 
