@@ -34,6 +34,8 @@
 // pass over the sequence is needed.
 //   dx = lam (1 - a) or lam;  da = lam (h_(t-1) - x) or lam h_(t-1);
 //   dg = da a (1 - a) or da;  dz = dy h silu'(z)
+#include <type_traits>
+
 #include "ss_layer.cuh"
 
 namespace selscan {
@@ -53,6 +55,19 @@ struct GlrParams {
     int64_t rows, dim, L, nck;
     int sigmoid, couple, vec;
 };
+
+// Calls f with the two flags as constants: what depends on them is then
+// decided once, not at every step.
+template <typename F>
+__device__ __forceinline__ void with_flags(bool sigmoid, bool couple, F f) {
+    if (sigmoid) {
+        if (couple) f(std::true_type{}, std::true_type{});
+        else f(std::true_type{}, std::false_type{});
+    } else {
+        if (couple) f(std::false_type{}, std::true_type{});
+        else f(std::false_type{}, std::false_type{});
+    }
+}
 
 // a, 1 - a of two gate inputs.  Fast: e = exp(-g) with its exponent held
 // below 2^126 (a NaN passes), so 1 / (1 + e) and e / (1 + e) are both finite
@@ -128,6 +143,12 @@ struct Pair {
     int cut;
 };
 
+// Vectors of a lane in the forward: 16 steps of bf16 halve what the scan over
+// the lanes costs a step (8 x 1536 x 2048: 37.5 us against 39), and would
+// take all the registers with fp32 (3 x 1000 x 4099: 45 us against 41).
+template <typename T>
+constexpr int kGlrVecs = sizeof(T) == 2 ? 2 : 1;
+
 // Where a row lies, in virtual steps from the 8-element boundary before it.
 struct Row {
     int64_t row, base, steps;
@@ -160,7 +181,7 @@ __device__ __forceinline__ void bounds_of(const Row &r, int64_t v, int &lo, int 
 template <typename Tin, typename Tout, bool kZ, bool kR, bool kShared, int kG>
 __global__ void __launch_bounds__(512) glr_fwd_kernel(const GlrParams p, int lanes) {
     constexpr bool kFast = sizeof(Tin) == 2;
-    constexpr int kVecs = 2, kE = kVecs * kV;  // steps of a lane
+    constexpr int kVecs = kGlrVecs<Tin>, kE = kVecs * kV;  // steps of a lane
     __shared__ Pair pairs[2][kMaxWarps];
     const int G = kG ? kG : lanes, lane = threadIdx.x & 31, in = lane & (G - 1);
     const int W = kShared ? (int)blockDim.x >> 5 : 1, w = kShared ? (int)threadIdx.x >> 5 : 0;
@@ -176,7 +197,7 @@ __global__ void __launch_bounds__(512) glr_fwd_kernel(const GlrParams p, int lan
     uint32_t ncut = 0;
     const auto fetch = [&](int64_t v) {
         ncut = 0;
-        if (vec && v > 0 && v + kE <= r.steps) {
+        if (vec && v >= r.shift && v + kE <= r.steps) {
 #pragma unroll
             for (int k = 0; k < kVecs; ++k) {
                 ng[k].load(g, v + k * kV);
@@ -205,14 +226,16 @@ __global__ void __launch_bounds__(512) glr_fwd_kernel(const GlrParams p, int lan
     for (int64_t v0 = 0; v0 < r.steps; v0 += stride, buf ^= 1) {
         const int64_t v = v0 + mine;
         float a[kE], b[kE];
+        with_flags(sigmoid, couple, [&](auto sig, auto cpl) {
 #pragma unroll
-        for (int i = 0; i < kE; i += 2) {
-            float2 a2, k2, b2 = nx[i / kV].pair(i % kV / 2);
-            gate2<kFast>(ng[i / kV].pair(i % kV / 2), sigmoid, a2, k2);
-            if (couple) b2 = mul2(k2, b2);
-            a[i] = a2.x, a[i + 1] = a2.y, b[i] = b2.x, b[i + 1] = b2.y;
-        }
-        const bool inner = v > 0 && v + kE <= r.steps;  // all of the lane's steps are the row's
+            for (int i = 0; i < kE; i += 2) {
+                float2 a2, k2, b2 = nx[i / kV].pair(i % kV / 2);
+                gate2<kFast>(ng[i / kV].pair(i % kV / 2), sig.value, a2, k2);
+                if (cpl.value) b2 = mul2(k2, b2);
+                a[i] = a2.x, a[i + 1] = a2.y, b[i] = b2.x, b[i + 1] = b2.y;
+            }
+        });
+        const bool inner = v >= r.shift && v + kE <= r.steps;  // all of the lane's steps are the row's
         if (!inner) {
 #pragma unroll
             for (int k = 0; k < kVecs; ++k) {
@@ -311,7 +334,7 @@ __global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p, int lan
     uint32_t ncut = 0;
     float nin = 0.f;
     const auto fetch = [&](int64_t v, int64_t start) {  // the lane's steps, and where the row's lanes begin
-        if (vec && v > 0 && v + kV <= r.steps) {
+        if (vec && v >= r.shift && v + kV <= r.steps) {
             ng.load(g, v);
             nx.load(x, v);
             nd.load(dy, v);
@@ -335,10 +358,15 @@ __global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p, int lan
     fetch(v0 + w * span + in * kV, v0 + w * span);
     for (; v0 >= 0; v0 -= stride, buf ^= 1) {
         const int64_t v = v0 + w * span + in * kV;
-        const bool inner = v > 0 && v + kV <= r.steps;
+        const bool inner = v >= r.shift && v + kV <= r.steps;
         float2 a[kV / 2], keep[kV / 2];
+        if (sigmoid) {
 #pragma unroll
-        for (int i = 0; i < kV / 2; ++i) gate2<kFast>(ng.pair(i), sigmoid, a[i], keep[i]);
+            for (int i = 0; i < kV / 2; ++i) gate2<kFast>(ng.pair(i), true, a[i], keep[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kV / 2; ++i) gate2<kFast>(ng.pair(i), false, a[i], keep[i]);
+        }
         if (!inner) {
             int lo, hi;
             bounds_of(r, v, lo, hi);
@@ -352,8 +380,7 @@ __global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p, int lan
         float2 xv[kV / 2], b[kV / 2], dh[kV / 2], dzv[kV / 2];
 #pragma unroll
         for (int i = 0; i < kV / 2; ++i) {
-            xv[i] = nx.pair(i);
-            b[i] = couple ? mul2(keep[i], xv[i]) : xv[i];
+            xv[i] = b[i] = nx.pair(i);
             dh[i] = nd.pair(i);
             if constexpr (kZ) {
                 // dy silu(z) and dy silu'(z) = dy s (1 + z (1 - s))
@@ -369,6 +396,10 @@ __global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p, int lan
                 dzv[i] = mul2(ds, fma2(zv, add2(both(1.f), neg2(s)), both(1.f)));
                 dh[i] = mul2(ds, zv);
             }
+        }
+        if (couple) {
+#pragma unroll
+            for (int i = 0; i < kV / 2; ++i) b[i] = mul2(keep[i], xv[i]);
         }
         const uint32_t cut = ncut;
         const float from_state = nin;
@@ -431,18 +462,20 @@ __global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p, int lan
         const int after = last - lane;  // the row's lanes behind this one
         float m = kR && after > 0 && (cuts & lanes_from(lane + 1, after)) ? Mx : fmaf(Amx, from, Mx);
         float ox[kV], og[kV];
+        with_flags(sigmoid, couple, [&](auto sig, auto cpl) {
 #pragma unroll
-        for (int i = kV / 2 - 1; i >= 0; --i) {
-            float2 lam;
-            lam.y = dh[i].y + m;
-            m = kR && (cut >> (2 * i + 1) & 1u) ? 0.f : a[i].y * lam.y;
-            lam.x = dh[i].x + m;
-            m = kR && (cut >> (2 * i) & 1u) ? 0.f : a[i].x * lam.x;
-            float2 da = mul2(lam, couple ? add2(before[i], neg2(xv[i])) : before[i]);
-            if (sigmoid) da = mul2(da, mul2(a[i], keep[i]));
-            if (couple) lam = mul2(lam, keep[i]);
-            ox[2 * i] = lam.x, ox[2 * i + 1] = lam.y, og[2 * i] = da.x, og[2 * i + 1] = da.y;
-        }
+            for (int i = kV / 2 - 1; i >= 0; --i) {
+                float2 lam;
+                lam.y = dh[i].y + m;
+                m = kR && (cut >> (2 * i + 1) & 1u) ? 0.f : a[i].y * lam.y;
+                lam.x = dh[i].x + m;
+                m = kR && (cut >> (2 * i) & 1u) ? 0.f : a[i].x * lam.x;
+                float2 da = mul2(lam, cpl.value ? add2(before[i], neg2(xv[i])) : before[i]);
+                if (sig.value) da = mul2(da, mul2(a[i], keep[i]));
+                if (cpl.value) lam = mul2(lam, keep[i]);
+                ox[2 * i] = lam.x, ox[2 * i + 1] = lam.y, og[2 * i] = da.x, og[2 * i + 1] = da.y;
+            }
+        });
         if (!r.there) continue;
         float oz[kV];
         if constexpr (kZ) {
@@ -506,7 +539,7 @@ GlrShape glr_shape(int64_t rows, int64_t L, int per_lane) {
 
 template <typename Tin, typename Tout, bool kZ, bool kR>
 cudaError_t launch_glr(bool back, cudaStream_t s, const GlrParams &p) {
-    const GlrShape q = glr_shape(p.rows, p.L, back ? kV : 2 * kV);
+    const GlrShape q = glr_shape(p.rows, p.L, back ? kV : kGlrVecs<Tin> * kV);
     constexpr int kThreads = 128;
     const int64_t per = kThreads / q.lanes;
     const unsigned grid = (unsigned)(q.warps > 1 ? p.rows : (p.rows + per - 1) / per);
