@@ -29,6 +29,8 @@
 // tests every tap against the starts; the others do not pay for it.
 #pragma once
 
+#include <type_traits>
+
 #include "ss_layer.cuh"
 
 namespace selscan {
@@ -47,6 +49,7 @@ struct ConvParams {
     int64_t main_blocks;  // forward: blocks of the outputs; the rest write the last state
     Divisor by_spans, by_dim;  // spans of a row, channels
     int small;            // the spans count in 31 bits (forward: of all rows; backward: of a channel)
+    int64_t chunks, groups;  // forward with starts: warps of spans to a row, groups of 8 channels to an entry
 };
 
 cudaError_t conv_fwd_f32_f32(int width, cudaStream_t s, ConvParams &p);
@@ -174,26 +177,28 @@ struct Window {
     }
 };
 
-// Bit k: a sequence starts at step t0 - (W-1) + k, for kBits steps.
-template <int W, int kBits>
-__device__ __forceinline__ uint32_t window_starts(const ConvParams &p, int64_t b, int64_t t0) {
-    uint32_t m = 0;
-    const int64_t first = t0 - (W - 1);
-#pragma unroll
-    for (int k = 0; k < kBits; k += kV) {
-        const int64_t t = first + k;
-        m |= start_bits(p.reset, b * p.L + t, p.batch * p.L, clamp8(-t), clamp8(p.L - t)) << k;
-    }
-    return kBits < 32 ? m & ((1u << kBits) - 1u) : m;
+// Bits of the starts at steps t0 + i of a span, i = first .. first + 7.
+__device__ __forceinline__ uint32_t span_starts(const ConvParams &p, int64_t b, const Span &s, int first) {
+    return start_bits(p.reset, b * p.L + s.t0 + first, p.batch * p.L, s.lo(first), s.hi(first));
 }
 
 // cut[j], bit k: a start lies between tap j of output k and the output's own
-// step (window positions k + j + 1 .. k + W - 1).
+// step (window positions k + j + 1 .. k + W - 1).  The result is the same in
+// all lanes: bit k is set where any of them has a tap cut in outputs k, k + 8.
+// Only those pairs of outputs test their taps (packed sequences of 500 steps
+// cut four pairs in a warp's 512 steps).
 template <int W>
-__device__ __forceinline__ void cuts_of(uint32_t m, uint32_t (&cut)[W]) {
+__device__ __forceinline__ uint32_t cuts_of(uint32_t m, uint32_t (&cut)[W]) {
     cut[W - 1] = 0;
 #pragma unroll
     for (int j = W - 2; j >= 0; --j) cut[j] = cut[j + 1] | m >> (j + 1);
+    return __reduce_or_sync(0xffffffffu, cut[0] | cut[0] >> kV);
+}
+// v, of a tap with these cuts of outputs k and k + 8, or zero behind a start.
+__device__ __forceinline__ float2 seen(float2 v, uint32_t cut, int k) {
+    if (cut >> k & 1u) v.x = 0.f;
+    if (cut >> (k + kV) & 1u) v.y = 0.f;
+    return v;
 }
 
 template <typename Tin, typename Tout, int W, bool kR>
@@ -210,11 +215,41 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(const ConvParams p) {
         put(static_cast<Tin *>(p.last), i, seen ? conv_input<Tin, W>(p, row, t) : 0.f);
         return;
     }
-    const int64_t q = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, nv = spans_of(L);
-    const bool there = q < rows * nv;  // (the threads behind stay for their warp's vote)
-    const uint32_t row = !there ? 0u : p.small ? divide((uint32_t)q, p.by_spans) : (uint32_t)(q / nv);
-    const uint32_t b = divide(row, p.by_dim), d = row - b * p.by_dim.d;
-    Span s = span_of(row * L, there ? q - row * nv : 0, L);
+    const int64_t nv = spans_of(L);
+    bool there;  // (the threads behind the end stay for their warp's vote)
+    uint32_t row, b, d;
+    int64_t v;
+    uint32_t m = 0;  // bit k: a sequence starts at step t0 - (W-1) + k
+    if constexpr (kR) {
+        // A warp's 32 spans of a row, and 8 channels that share their starts
+        // in a block: the mask's bytes become bits once for all of them.
+        constexpr int kAhead = 16, kWords = 32 * kSpan / 32 + 2;  // from 16 steps before the warp's spans
+        __shared__ uint32_t bits[kWords];
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int64_t chunk = blockIdx.x % p.chunks, group = blockIdx.x / p.chunks;
+        b = (uint32_t)(group / p.groups);
+        d = (uint32_t)(group - (int64_t)b * p.groups) * 8 + warp;
+        const int64_t first = chunk * 32 * kSpan - kAhead;
+        for (int k = warp; k < kWords; k += 8) {
+            const int64_t t = first + k * 32 + lane;
+            const uint32_t w = __ballot_sync(0xffffffffu, t >= 0 && t < L && __ldg(p.reset + b * L + max(t, (int64_t)0)) != 0);
+            if (lane == 0) bits[k] = w;
+        }
+        __syncthreads();
+        v = chunk * 32 + lane;
+        there = d < p.dim && v < nv;
+        if (!there) d = 0, v = 0;
+        row = b * (uint32_t)p.dim + d;
+        const int at = kAhead + lane * kSpan - (int)(row * L & (kV - 1)) - (W - 1);
+        if (there) m = __funnelshift_r(bits[at >> 5], bits[(at >> 5) + 1], at & 31) & ((1u << (W - 1 + kSpan)) - 1u);
+    } else {
+        const int64_t q = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+        there = q < rows * nv;
+        row = !there ? 0u : p.small ? divide((uint32_t)q, p.by_spans) : (uint32_t)(q / nv);
+        b = divide(row, p.by_dim), d = row - b * p.by_dim.d;
+        v = there ? q - row * nv : 0;
+    }
+    Span s = span_of(row * L, v, L);
     if (!there) s.tail = -kSpan;
     const bool whole = p.vec && s.head >= 0 && s.tail >= kSpan, inner = whole && s.head >= kV;
     float w[W];
@@ -224,26 +259,15 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(const ConvParams p) {
     Window<Tin, W, 2> x;
     x.load(p, static_cast<const Tin *>(p.x), s, row, n, inner);
     float2 out[kV];
-    uint32_t m = 0;
-    if constexpr (kR) m = window_starts<W, W - 1 + kSpan>(p, b, s.t0);
-    if (kR && __any_sync(0xffffffffu, m != 0)) {
-        uint32_t cut[W];
-        cuts_of<W>(m, cut);
+    uint32_t cut[W];
+    const uint32_t slow = kR ? cuts_of<W>(m, cut) : 0u;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            out[i] = both(bias);
+    for (int i = 0; i < kV; ++i) {
+        out[i] = both(bias);
+        if (kR && (slow >> i & 1u)) {
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                float2 v = x.v[i + j];
-                if (cut[j] >> i & 1u) v.x = 0.f;
-                if (cut[j] >> (i + kV) & 1u) v.y = 0.f;
-                out[i] = fma2(both(w[j]), v, out[i]);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            out[i] = both(bias);
+            for (int j = 0; j < W; ++j) out[i] = fma2(both(w[j]), seen(x.v[i + j], cut[j], i), out[i]);
+        } else {
 #pragma unroll
             for (int j = 0; j < W; ++j) out[i] = fma2(both(w[j]), x.v[i + j], out[i]);
         }
@@ -330,6 +354,7 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
 
     __shared__ Slots<Tin> xs[2];
     __shared__ Slots<Tout> gs[2];
+    __shared__ uint32_t starts[kR ? kConvBwdThreads + 2 : 1];
     const int t = threadIdx.x;
     const int64_t nv = spans_of(L), total = p.batch * nv, stride = (int64_t)nblk * blockDim.x;
     // Span q of the channel; one behind the last has no step.
@@ -371,9 +396,22 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
         } else {
             cp_async_wait_all();
         }
-        __syncthreads();
         int64_t b;
         const Span s = place(q, b);
+        uint32_t m = 0;  // bit k: a sequence starts at step t0 - (W-1) + k
+        if constexpr (kR) {
+            // each thread's own 16 steps, and those of its neighbours
+            m = span_starts(p, b, s, 0) | span_starts(p, b, s, kV) << kV;
+            starts[t + 1] = m;
+            if (t == 0) starts[0] = span_starts(p, b, s, -kV) << kV;
+            if (t == kConvBwdThreads - 1) starts[t + 2] = span_starts(p, b, s, kSpan);
+        }
+        __syncthreads();
+        if constexpr (kR) {
+            const uint32_t before = s.head > 0 ? starts[t] : 0u, behind = s.tail > kSpan ? starts[t + 2] : 0u;
+            m = (before & 0xffffu) >> (kSpan - (W - 1)) | m << (W - 1) | behind << (W - 1 + kSpan);
+            m &= (1u << (2 * (W - 1) + kSpan)) - 1u;
+        }
         const int64_t row = b * p.dim + d;
         const bool whole = vec && s.head >= 0 && s.tail >= kSpan;
         constexpr int kOut = kV + W - 1;  // pairs of outputs: the thread's steps and W - 1 behind
@@ -399,60 +437,36 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
             for (int k = 0; k < kOut; ++k) slope[k] = make_float2(u[k / kV][k % kV], u[k / kV + 1][k % kV]);
         }
         __syncthreads();  // this half may be filled again
-        uint32_t m = 0;
-        if constexpr (kR) m = window_starts<W, 2 * (W - 1) + kSpan>(p, b, s.t0);
-        const bool cutting = kR && __any_sync(0xffffffffu, m != 0);
         uint32_t cut[W];
-        cuts_of<W>(m, cut);
-        const auto tap = [&](float2 v, int j, int k) {  // v, of tap j of outputs k, k + 8, or zero behind a start
-            if (kR && (cut[j] >> k & 1u)) v.x = 0.f;
-            if (kR && (cut[j] >> (k + kV) & 1u)) v.y = 0.f;
-            return v;
-        };
-        if (silu) {
-            if (cutting) {
-#pragma unroll
-                for (int k = 0; k < kOut; ++k) {
-                    float2 pre = both(bias);
-#pragma unroll
-                    for (int j = 0; j < W; ++j) pre = fma2(both(w[j]), tap(win.v[k + j], j, k), pre);
-                    slope[k] = conv_slope<kFast>(pre, slope[k]);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < kOut; ++k) {
-                    float2 pre = both(bias);
-#pragma unroll
-                    for (int j = 0; j < W; ++j) pre = fma2(both(w[j]), win.v[k + j], pre);
-                    slope[k] = conv_slope<kFast>(pre, slope[k]);
-                }
-            }
-        }
+        const uint32_t slow = kR ? cuts_of<W>(m, cut) : 0u;
+        // Output by output: p, q, and what q adds to the steps of its taps and
+        // to the sums (of the thread's own outputs, k < 8).  Tap j of output k
+        // reads window position k + j, step k + j - (W-1) of the thread.
         float2 g[kV];
-        // output i + j reads step i with its tap W-1-j; the sums take the thread's own outputs
-        if (cutting) {
 #pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                g[i] = both(0.f);
+        for (int i = 0; i < kV; ++i) g[i] = both(0.f);
+        const auto output = [&](int k, auto cutting) {
+            float2 tap[W], sl = slope[k];
 #pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    g[i] = fma2(both(w[W - 1 - j]), tap(slope[i + j], W - 1 - j, i + j), g[i]);
-                    const float2 xv = tap(win.v[i + j], j, i);
-                    sum2[j] = fma2(slope[i], xv, sum2[j]);
-                }
-                sum2[W] = add2(sum2[W], slope[i]);
+            for (int j = 0; j < W; ++j) tap[j] = cutting.value ? seen(win.v[k + j], cut[j], k) : win.v[k + j];
+            if (silu) {
+                float2 pre = both(bias);
+#pragma unroll
+                for (int j = 0; j < W; ++j) pre = fma2(both(w[j]), tap[j], pre);
+                sl = conv_slope<kFast>(pre, sl);
             }
-        } else {
 #pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                g[i] = both(0.f);
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    g[i] = fma2(both(w[W - 1 - j]), slope[i + j], g[i]);
-                    sum2[j] = fma2(slope[i], win.v[i + j], sum2[j]);
-                }
-                sum2[W] = add2(sum2[W], slope[i]);
+            for (int j = 0; j < W; ++j) {
+                const int i = k + j - (W - 1);
+                if (i >= 0 && i < kV) g[i] = fma2(both(w[j]), cutting.value ? seen(sl, cut[j], k) : sl, g[i]);
+                if (k < kV) sum2[j] = fma2(sl, tap[j], sum2[j]);
             }
+            if (k < kV) sum2[W] = add2(sum2[W], sl);
+        };
+#pragma unroll
+        for (int k = 0; k < kOut; ++k) {
+            if (kR && (slow >> k & 1u)) output(k, std::true_type{});
+            else output(k, std::false_type{});
         }
         if (p.dlast && there && s.t0 + kSpan > L - (W - 1)) {  // the last state's elements are inputs too
             bool seen = true;

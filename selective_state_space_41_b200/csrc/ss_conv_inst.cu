@@ -21,6 +21,10 @@ cudaError_t fwd(cudaStream_t s, ConvParams &p) {
     p.main_blocks = (spans + 255) / 256;
     p.small = spans <= INT_MAX;
     p.by_spans = divisor_of(spans_of(p.L)), p.by_dim = divisor_of(p.dim);
+    if (p.reset) {
+        p.chunks = (spans_of(p.L) + 31) / 32, p.groups = (p.dim + 7) / 8;
+        p.main_blocks = p.batch * p.groups * p.chunks;
+    }
     const int64_t tail = p.last ? (p.batch * p.dim * (W - 1) + 255) / 256 : 0;
     if (p.main_blocks + tail > INT_MAX) return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)(p.main_blocks + tail);

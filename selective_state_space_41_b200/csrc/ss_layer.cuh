@@ -181,13 +181,12 @@ inline Divisor divisor_of(int64_t d) {
 }
 __device__ __forceinline__ uint32_t divide(uint32_t n, const Divisor &v) { return v.mul ? __umulhi(n, v.mul) >> v.shift : n; }
 
-// Bit i: whether byte i of the pair of words is nonzero.
-__device__ __forceinline__ uint32_t nonzero_bytes(uint32_t lo, uint32_t hi) {
-    // one per nonzero byte, then the four ones gathered into bits 24..27 (the
-    // ten partial products below them fall on different bits: no carries)
-    const uint32_t a = (__vminu4(lo, 0x01010101u) * 0x01020408u) >> 24;
-    const uint32_t b = (__vminu4(hi, 0x01010101u) * 0x01020408u) >> 24;
-    return (a & 15u) | ((b & 15u) << 4);
+// Bits 0..3: whether bytes 0..3 of a word are nonzero.  The sum carries into
+// a byte's top bit unless its low seven are zero; the product gathers the four
+// ones into bits 24..27 (its ten partial products fall on different bits).
+__device__ __forceinline__ uint32_t nonzero_bytes(uint32_t w) {
+    const uint32_t top = (((w & 0x7f7f7f7fu) + 0x7f7f7f7fu) | w) & 0x80808080u;
+    return (top >> 7) * 0x01020408u >> 24;
 }
 
 // Bits lo..hi-1 of the start mask of eight steps from byte m of `reset`, whose
@@ -203,7 +202,7 @@ __device__ __forceinline__ uint32_t start_bits(const uint8_t *reset, int64_t m, 
         const uint2 u = __ldg(q), v = __ldg(q + 1);
         const unsigned long long a = ((unsigned long long)u.y << 32) | u.x, b = ((unsigned long long)v.y << 32) | v.x;
         const unsigned long long x = off ? (a >> (8 * off)) | (b << (64 - 8 * off)) : a;
-        return nonzero_bytes((uint32_t)x, (uint32_t)(x >> 32)) & keep;
+        return (nonzero_bytes((uint32_t)x) & 15u | nonzero_bytes((uint32_t)(x >> 32)) << 4) & keep;
     }
     uint32_t bits = 0;
     for (int i = lo; i < hi; ++i)
