@@ -315,8 +315,6 @@ struct Slots {
             for (int k = 0; k < kQ; ++k) to[k] = make_uint4(v.w[4 * k], v.w[4 * k + 1], v.w[4 * k + 2], v.w[4 * k + 3]);
         }
     }
-    // It, with elements [lo, hi) kept (the others were not copied, or are
-    // those of a neighbouring row).
     __device__ __forceinline__ void read(Vec8<T> &v, int i) const {
 #pragma unroll
         for (int k = 0; k < kQ; ++k) {
@@ -324,14 +322,16 @@ struct Slots {
             v.w[4 * k] = u.x, v.w[4 * k + 1] = u.y, v.w[4 * k + 2] = u.z, v.w[4 * k + 3] = u.w;
         }
     }
-    __device__ __forceinline__ void read(Vec8<T> &v, int i, int lo, int hi) const {
-        read(v, i);
-        if (lo > 0 || hi < kV) {
-            if (hi > lo) v.keep(lo, hi);
-            else v.clear();
-        }
-    }
 };
+
+// Clears what of a vector is not in the row (it was not copied, or belongs to
+// a neighbouring row): all of it or nothing where rows are whole vectors.
+template <typename T>
+__device__ __forceinline__ void trim(Vec8<T> &v, const Span &s, int i, bool whole_rows) {
+    const int lo = s.lo(i), hi = s.hi(i);
+    if (hi <= lo) v.clear();
+    else if (!whole_rows && (lo > 0 || hi < kV)) v.keep(lo, hi);
+}
 
 template <typename Tin, typename Tout, int W, bool kR>
 __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const ConvParams p, int nblk) {
@@ -365,9 +365,8 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
         if (!there) s.tail = -kSpan;
         return s;
     };
-    const auto fill = [&](int64_t q, int buf) {
-        int64_t b;
-        const Span s = place(q, b);
+    const bool whole_rows = L % kV == 0;
+    const auto fill = [&](const Span &s, int buf) {
         if (vec && s.head >= 0 && s.tail >= kSpan) {
             xs[buf].fill_whole(t, x + s.e);
             gs[buf].fill_whole(t, dy + s.e);
@@ -386,18 +385,20 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
         cp_async_commit();
     };
     int buf = 0;
-    fill((int64_t)rank * blockDim.x + t, 0);
+    int64_t b, next_b;
+    Span s, next = place((int64_t)rank * blockDim.x + t, next_b);
+    fill(next, 0);
     for (int64_t q0 = (int64_t)rank * blockDim.x; q0 < total; q0 += stride, buf ^= 1) {
         const int64_t q = q0 + t;
         const bool there = q < total;
+        s = next, b = next_b;
         if (q0 + stride < total) {
-            fill(q + stride, buf ^ 1);
+            next = place(q + stride, next_b);
+            fill(next, buf ^ 1);
             cp_async_wait_one();
         } else {
             cp_async_wait_all();
         }
-        int64_t b;
-        const Span s = place(q, b);
         uint32_t m = 0;  // bit k: a sequence starts at step t0 - (W-1) + k
         if constexpr (kR) {
             // each thread's own 16 steps, and those of its neighbours
@@ -420,16 +421,15 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
         {
             Vec8<Tin> v[4];
             Vec8<Tout> u[3];
-            if (s.head >= kV && s.tail >= kSpan + kV) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) xs[buf].read(v[i], 2 * t + 1 + i);
+            for (int i = 0; i < 4; ++i) xs[buf].read(v[i], 2 * t + 1 + i);
 #pragma unroll
-                for (int i = 0; i < 3; ++i) gs[buf].read(u[i], 2 * t + 2 + i);
-            } else {
+            for (int i = 0; i < 3; ++i) gs[buf].read(u[i], 2 * t + 2 + i);
+            if (s.head < kV || s.tail < kSpan + kV) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) xs[buf].read(v[i], 2 * t + 1 + i, s.lo((i - 1) * kV), s.hi((i - 1) * kV));
+                for (int i = 0; i < 4; ++i) trim(v[i], s, (i - 1) * kV, whole_rows);
 #pragma unroll
-                for (int i = 0; i < 3; ++i) gs[buf].read(u[i], 2 * t + 2 + i, s.lo(i * kV), s.hi(i * kV));
+                for (int i = 0; i < 3; ++i) trim(u[i], s, i * kV, whole_rows);
             }
             win.take(p, v, s, row);
             // outputs outside the row have dy = 0, and with it no part in anything

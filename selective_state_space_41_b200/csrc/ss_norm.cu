@@ -1238,6 +1238,7 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const float *part, int6
                                                          float *dbias) {
     __shared__ float sm[32][33];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched ahead: the parts are there from here on
     const int64_t c = (int64_t)blockIdx.x * 32 + tx;
     float s = 0.f;
     if (c < 2 * dim) {
@@ -1332,10 +1333,14 @@ NormPlan norm_plan(const ss_desc *desc, bool vec, bool back) {
         if (pl.warps < 2) pl.warps = 2;  // a thread for each step of the tile
         pl.V = !vec ? 1 : desc->in_dtype == SS_BF16 ? 8 : 4;
         const int64_t wide = pl.V == 8 ? 64 : 32, count = (n + wide - 1) / wide;
-        const int64_t resident = (sms * (pl.max_warps == 8 ? 2 : 1) + nblk - 1) / nblk;
-        const int64_t rounds = (count + resident - 1) / resident;
+        // Clusters that run at the same time: a cluster lies within one of the
+        // eight groups of SMs, which are not all of a size, hence a margin (one
+        // cluster too many runs alone after all the others: 71 us, not 55, for
+        // 3 x 1000 x 4099 fp32).
+        const int64_t resident = nblk <= 2 ? sms * (pl.max_warps == 8 ? 2 : 1) / nblk
+                                           : sms / 8 * (pl.max_warps == 8 ? 2 : 1) / nblk * 8 * 92 / 100;
         pl.blocks = count;
-        pl.parts = rounds > 0 ? (count + rounds - 1) / rounds : 0;
+        pl.parts = count < resident ? count : resident;
         return pl;
     }
     pl.kind = kStepsWide;
@@ -1509,8 +1514,18 @@ ss_status ss_norm_bwd(const ss_desc *desc, const void *x, const float *weight, c
     const NormPlan pl = norm_plan(desc, norm_vec(desc, {x, dy, dx}, {weight}), true);  // the workspace is aligned
     cudaError_t e = SS_LAYER_DISPATCH(desc, dispatch_norm)(true, pl, s, p);
     if (e == cudaSuccess && p.sums) {
-        norm_sums_kernel<<<(unsigned)((2 * p.dim + 31) / 32), 1024, 0, s>>>(p.part, pl.parts, p.dim, dweight, dbias);
-        e = cudaGetLastError();
+        // set up while the blocks of the kernel before it are still ending
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)((2 * p.dim + 31) / 32));
+        cfg.blockDim = dim3(1024);
+        cfg.stream = s;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        const float *part = p.part;
+        e = cudaLaunchKernelEx(&cfg, norm_sums_kernel, part, pl.parts, p.dim, dweight, dbias);
     }
     return status_of(e);
 }
