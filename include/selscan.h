@@ -2,7 +2,10 @@
  * libselscan -- the selective scan of Mamba on NVIDIA B200 (sm_100a), C ABI:
  * the forward (from a zero or a given state, optionally with sequence starts
  * inside the rows), one-step decoding, and the backward (gradients of every
- * input, with or without sequence starts).
+ * input, with or without sequence starts); and the operators around it in a
+ * layer: normalisation over the channels, the causal depthwise convolution
+ * and the gated linear recurrence, each forward, backward and (the latter
+ * two) as a decoding step.
  *
  * The operation is the selective scan of Mamba as the selective_scan_ref
  * walkthrough defines it ("Mamba代码实战：手把手教你用PyTorch复现选择性扫描核心逻辑

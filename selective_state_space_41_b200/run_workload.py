@@ -3,6 +3,8 @@
     python -m selective_state_space_41_b200.run_workload NAME [--batch B]
         [--repeat K] [--lanes G] [--split S] [--warps W] [--segments P]
         [--dt-rank R] [--backward] [--backward-ckpt]
+    python -m selective_state_space_41_b200.run_workload NAME --op norm|conv|recurrence
+        [--batch B] [--repeat K] [--width W] [--rms] [--backward]
 
 Draws the workload's seeded inputs (optionally only its first B batch
 entries, to keep a capture small), moves them to ``cuda:0`` and calls
@@ -11,13 +13,42 @@ shape given, zeros meaning the heuristic's choice.  A workspace is passed
 when the shape uses sequence segments.  ``--backward`` calls ``ss_bwd`` (all
 gradients, a seeded dy, its own plan) K times instead; ``--backward-ckpt``
 calls ``ss_fwd_ckpt`` once, then ``ss_bwd_ckpt`` from its checkpoints K
-times.  Prints ``ok`` after a final synchronize.
+times.
+
+``--op`` runs one of the operators around the scan on the workload's u (and,
+for the recurrence, delta as the gate and z as the output gate) with seeded
+parameters: the normalisation over the channels, the causal convolution with
+silu, or the coupled gated recurrence, forward or ``--backward``.  Prints
+``ok`` after a final synchronize.
 """
 import argparse
 
 import torch
 
-from . import gen, selscan, workloads as W
+from . import gen, layer_ops, selscan, workloads as W
+
+
+def run_layer_op(a, w):
+    """K calls of the operator ``a.op`` on workload ``w``."""
+    d = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in W.make_layer_inputs(w, a.width).items()}
+    u = d["u"]
+    dy = gen.fill(tuple(u.shape), w.dtype, w.seed, 9).cuda() if a.backward else None
+    if a.op == "norm":
+        bias = None if a.rms else d["norm_bias"]
+        _, mean, rstd = layer_ops.layer_norm_fwd(u, d["norm_weight"], bias, rms=a.rms, return_stats=True)
+        forward = lambda: layer_ops.layer_norm_fwd(u, d["norm_weight"], bias, rms=a.rms)  # noqa: E731
+        backward = lambda: layer_ops.layer_norm_bwd(u, dy, rstd, mean, d["norm_weight"], bias, a.rms)  # noqa: E731
+    elif a.op == "conv":
+        kw = dict(bias=d["conv_bias"], silu=True)
+        forward = lambda: layer_ops.causal_conv_fwd(u, d["conv_weight"], **kw)  # noqa: E731
+        backward = lambda: layer_ops.causal_conv_bwd(u, d["conv_weight"], dy, **kw)  # noqa: E731
+    else:
+        kw = dict(z=d["z"], couple=True)
+        _, ckpt = layer_ops.gated_recurrence_fwd(u, d["delta"], return_ckpt=True, **kw)
+        forward = lambda: layer_ops.gated_recurrence_fwd(u, d["delta"], **kw)  # noqa: E731
+        backward = lambda: layer_ops.gated_recurrence_bwd(u, d["delta"], dy, ckpt, **kw)  # noqa: E731
+    for _ in range(a.repeat):
+        (backward if a.backward else forward)()
 
 
 def main(argv=None):
@@ -32,10 +63,18 @@ def main(argv=None):
     ap.add_argument("--dt-rank", type=int, default=0)
     ap.add_argument("--backward", action="store_true")
     ap.add_argument("--backward-ckpt", action="store_true")
+    ap.add_argument("--op", choices=("scan", "norm", "conv", "recurrence"), default="scan")
+    ap.add_argument("--width", type=int, default=4)
+    ap.add_argument("--rms", action="store_true")
     a = ap.parse_args(argv)
     w = W.WORKLOADS[a.name]
     if a.batch:
         w = W.with_shape(w, batch=a.batch)
+    if a.op != "scan":
+        run_layer_op(a, w)
+        torch.cuda.synchronize()
+        print("ok")
+        return
     inp = W.make_dtproj_inputs(w, a.dt_rank) if a.dt_rank else W.make_inputs(w)
     d = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in inp.items()}
     y = torch.empty(d["u"].shape, dtype=w.out_dtype or w.dtype, device="cuda")

@@ -18,7 +18,8 @@ import torch
 from . import gen
 
 # Philox stream ids, one per operand.
-STREAM = {"u": 1, "delta": 2, "B": 3, "C": 4, "z": 5, "D": 6, "delta_bias": 7, "delta_r": 11, "W_dt": 12}
+STREAM = {"u": 1, "delta": 2, "B": 3, "C": 4, "z": 5, "D": 6, "delta_bias": 7, "delta_r": 11, "W_dt": 12,
+          "norm_weight": 13, "norm_bias": 14, "conv_weight": 15, "conv_bias": 16}
 
 # dt_rank of the dt_proj form for a layer of model width d_model: the pages
 # give dt_rank = 'auto' without a rule ("Mamba-minimal项目解析", 1. ModelArgs);
@@ -144,4 +145,18 @@ def make_dtproj_inputs(w: Workload, dt_rank: int, pin: bool = False) -> dict:
     out["delta_r"] = gen.fill((w.batch, dt_rank, w.seqlen), w.dtype, w.seed, STREAM["delta_r"], gen.NORMAL,
                               0.0, 1.0, pin)
     out["W_dt"] = gen.fill((w.dim, dt_rank), w.dtype, w.seed, STREAM["W_dt"], gen.UNIFORM, -bound, bound, pin)
+    return out
+
+
+def make_layer_inputs(w: Workload, width: int = 4, pin: bool = False) -> dict:
+    """make_inputs(w) plus the parameters of the operators around the scan:
+    norm_weight ~ N(1, 0.1), norm_bias ~ N(0, 0.1) (D,); conv_weight (D,
+    width) ~ N(0, 1 / width), conv_bias (D,) ~ N(0, 0.1); all float32.  The
+    recurrence takes u as its input, delta as its gate and z as its output
+    gate."""
+    out = make_inputs(w, pin=pin)
+    for name, shape, mean, dev in (("norm_weight", (w.dim,), 1.0, 0.1), ("norm_bias", (w.dim,), 0.0, 0.1),
+                                   ("conv_weight", (w.dim, width), 0.0, width ** -0.5),
+                                   ("conv_bias", (w.dim,), 0.0, 0.1)):
+        out[name] = gen.fill(shape, torch.float32, w.seed, STREAM[name], gen.NORMAL, mean, dev, pin)
     return out
