@@ -109,7 +109,7 @@ __device__ __forceinline__ float2 conv_slope(float2 pre, float2 dy) {
     } else {
         s = make_float2(1.f / (1.f + expf(-pre.x)), 1.f / (1.f + expf(-pre.y)));
     }
-    return mul2(dy, mul2(s, fma2(pre, add2(both(1.f), neg2(s)), both(1.f))));
+    return mul2(dy, mul2(s, fma2(pre, sub2(both(1.f), s), both(1.f))));
 }
 
 constexpr int kSpan = 16;  // steps of a thread

@@ -76,7 +76,7 @@ template <bool kFast>
 __device__ __forceinline__ void gate2(float2 g, bool sigmoid, float2 &a, float2 &keep) {
     if (!sigmoid) {
         a = g;
-        keep = add2(both(1.f), neg2(g));
+        keep = sub2(both(1.f), g);
     } else if constexpr (kFast) {
         float2 t = mul2(g, both(-kLog2e));
         asm("min.NaN.f32 %0, %1, %2;" : "=f"(t.x) : "f"(t.x), "f"(126.f));
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p, int lan
                     s = make_float2(1.f / (1.f + expf(-zv.x)), 1.f / (1.f + expf(-zv.y)));
                 }
                 const float2 ds = mul2(dh[i], s);
-                dzv[i] = mul2(ds, fma2(zv, add2(both(1.f), neg2(s)), both(1.f)));
+                dzv[i] = mul2(ds, fma2(zv, sub2(both(1.f), s), both(1.f)));
                 dh[i] = mul2(ds, zv);
             }
         }
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p, int lan
                 m = kR && (cut >> (2 * i + 1) & 1u) ? 0.f : a[i].y * lam.y;
                 lam.x = dh[i].x + m;
                 m = kR && (cut >> (2 * i) & 1u) ? 0.f : a[i].x * lam.x;
-                float2 da = mul2(lam, cpl.value ? add2(before[i], neg2(xv[i])) : before[i]);
+                float2 da = mul2(lam, cpl.value ? sub2(before[i], xv[i]) : before[i]);
                 if (sig.value) da = mul2(da, mul2(a[i], keep[i]));
                 if (cpl.value) lam = mul2(lam, keep[i]);
                 ox[2 * i] = lam.x, ox[2 * i + 1] = lam.y, og[2 * i] = da.x, og[2 * i + 1] = da.y;

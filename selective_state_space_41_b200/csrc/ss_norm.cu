@@ -257,11 +257,28 @@ __global__ void __launch_bounds__(512) norm_rows_bwd_kernel(const NormParams p, 
         for (int i = 0; i < kV / 2; ++i) dw[k][i] = db[k][i] = both(0.f);
     }
     int buf = 0;
-    for (int64_t row = (int64_t)blockIdx.x * groups + group; row < p.batch; row += step, buf ^= 1) {
-        Vec8<Tin> x[kNv];
-        Vec8<Tout> dy[kNv];
-        load_row<Tin, kNv, kVec>(x, static_cast<const Tin *>(p.x) + row * p.dim, t, T, dim);
-        load_row<Tout, kNv, kVec>(dy, static_cast<const Tout *>(p.dy) + row * p.dim, t, T, dim);
+    int64_t row = (int64_t)blockIdx.x * groups + group;
+    // The next row is on its way while one is worked on, where the registers
+    // hold both (8192 rows of 4096 bf16: 64 us against 76 without).
+    constexpr bool kAhead = kNv <= (kVec ? 2 : 1);
+    Vec8<Tin> x[kNv], nx[kNv];
+    Vec8<Tout> dy[kNv], ny[kNv];
+    if (kAhead && row < p.batch) {
+        load_row<Tin, kNv, kVec>(nx, static_cast<const Tin *>(p.x) + row * p.dim, t, T, dim);
+        load_row<Tout, kNv, kVec>(ny, static_cast<const Tout *>(p.dy) + row * p.dim, t, T, dim);
+    }
+    for (; row < p.batch; row += step, buf ^= 1) {
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int k = 0; k < kNv; ++k) x[k] = nx[k], dy[k] = ny[k];
+            if (row + step < p.batch) {
+                load_row<Tin, kNv, kVec>(nx, static_cast<const Tin *>(p.x) + (row + step) * p.dim, t, T, dim);
+                load_row<Tout, kNv, kVec>(ny, static_cast<const Tout *>(p.dy) + (row + step) * p.dim, t, T, dim);
+            }
+        } else {
+            load_row<Tin, kNv, kVec>(x, static_cast<const Tin *>(p.x) + row * p.dim, t, T, dim);
+            load_row<Tout, kNv, kVec>(dy, static_cast<const Tout *>(p.dy) + row * p.dim, t, T, dim);
+        }
         const float2 nm = both(p.mean_in ? -__ldg(p.mean_in + row) : 0.f);
         const float rstd = __ldg(p.rstd_in + row);
         // elements that are not there have dy = 0, and count in no sum
@@ -964,15 +981,15 @@ __global__ void __launch_bounds__(32 * kTileWarps, 2) norm_tile_fwd_kernel(const
 #pragma unroll
             for (int k = 0; k < G::kStats; ++k) {
                 const float2 e = mul2(D[k], both(inv_n));
-                S[k] = fma2(neg2(D[k]), e, S[k]);
-                m[k] = add2(e, neg2(np[k]));
+                S[k] = fma2(mul2(D[k], both(-1.f)), e, S[k]);
+                m[k] = sub2(e, np[k]);
                 mw[k] = mul2(m[k], both(nt));
             }
             step_sums(mw);
 #pragma unroll
             for (int k = 0; k < G::kStats; ++k) {
                 D[k] = mul2(mw[k], both(inv_w));
-                const float2 d = add2(m[k], neg2(D[k]));
+                const float2 d = sub2(m[k], D[k]);
                 S[k] = fma2(mul2(d, both(nt)), d, S[k]);
             }
         } else {
@@ -1238,7 +1255,6 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const float *part, int6
                                                          float *dbias) {
     __shared__ float sm[32][33];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched ahead: the parts are there from here on
     const int64_t c = (int64_t)blockIdx.x * 32 + tx;
     float s = 0.f;
     if (c < 2 * dim) {
@@ -1514,18 +1530,8 @@ ss_status ss_norm_bwd(const ss_desc *desc, const void *x, const float *weight, c
     const NormPlan pl = norm_plan(desc, norm_vec(desc, {x, dy, dx}, {weight}), true);  // the workspace is aligned
     cudaError_t e = SS_LAYER_DISPATCH(desc, dispatch_norm)(true, pl, s, p);
     if (e == cudaSuccess && p.sums) {
-        // set up while the blocks of the kernel before it are still ending
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)((2 * p.dim + 31) / 32));
-        cfg.blockDim = dim3(1024);
-        cfg.stream = s;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        const float *part = p.part;
-        e = cudaLaunchKernelEx(&cfg, norm_sums_kernel, part, pl.parts, p.dim, dweight, dbias);
+        norm_sums_kernel<<<(unsigned)((2 * p.dim + 31) / 32), 1024, 0, s>>>(p.part, pl.parts, p.dim, dweight, dbias);
+        e = cudaGetLastError();
     }
     return status_of(e);
 }
