@@ -9,7 +9,6 @@ namespace {
 // the new one takes the last.
 template <typename Tin, typename Tout>
 __global__ void __launch_bounds__(128) conv_step_kernel(const ConvParams p) {
-    constexpr bool kFast = sizeof(Tin) == 2;
     const int64_t row = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (row >= p.batch * p.dim) return;
     const int W = p.width;
@@ -33,7 +32,7 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvParams p) {
     for (int j = 1; j < kMaxWidth; ++j)
         if (j == W - 1) acc = fmaf(wv[j], xv, acc);
     put(state, W - 2, xv);
-    put(static_cast<Tout *>(p.y), row, p.silu ? silu2<kFast>(both(acc)).x : acc);
+    put(static_cast<Tout *>(p.y), row, p.silu ? silu2(both(acc)).x : acc);
 }
 
 template <typename Tin, typename Tout>

@@ -88,29 +88,8 @@ __device__ __forceinline__ float conv_at(const ConvParams &p, int64_t row, int64
     return acc;
 }
 
-// p (1 / (1 + exp(-p))): exp(-p) may overflow, to a result of zero.
-template <bool kFast>
-__device__ __forceinline__ float2 silu2(float2 v) {
-    if constexpr (kFast) {
-        const float2 t = mul2(v, both(-kLog2e)), u = add2(make_float2(sfu_exp2(t.x), sfu_exp2(t.y)), both(1.f));
-        return mul2(v, make_float2(sfu_rcp(u.x), sfu_rcp(u.y)));
-    } else {
-        return make_float2(v.x / (1.f + expf(-v.x)), v.y / (1.f + expf(-v.y)));
-    }
-}
-
-// dy silu'(p) = dy s (1 + p (1 - s)).
-template <bool kFast>
-__device__ __forceinline__ float2 conv_slope(float2 pre, float2 dy) {
-    float2 s;
-    if constexpr (kFast) {
-        const float2 t = mul2(pre, both(-kLog2e)), u = add2(make_float2(sfu_exp2(t.x), sfu_exp2(t.y)), both(1.f));
-        s = make_float2(sfu_rcp(u.x), sfu_rcp(u.y));
-    } else {
-        s = make_float2(1.f / (1.f + expf(-pre.x)), 1.f / (1.f + expf(-pre.y)));
-    }
-    return mul2(dy, mul2(s, fma2(pre, sub2(both(1.f), s), both(1.f))));
-}
+// dy silu'(p).
+__device__ __forceinline__ float2 conv_slope(float2 pre, float2 dy) { return mul2(dy, silu_slope2(pre, sigmoid2(pre))); }
 
 constexpr int kSpan = 16;  // steps of a thread
 
@@ -203,7 +182,6 @@ __device__ __forceinline__ float2 seen(float2 v, uint32_t cut, int k) {
 
 template <typename Tin, typename Tout, int W, bool kR>
 __global__ void __launch_bounds__(256) conv_fwd_kernel(const ConvParams p) {
-    constexpr bool kFast = sizeof(Tin) == 2;
     const int64_t L = p.L, rows = p.batch * p.dim, n = rows * L;
     if (blockIdx.x >= p.main_blocks) {
         // the last W - 1 inputs, those of the last sequence alone
@@ -274,7 +252,7 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(const ConvParams p) {
     }
     if (p.silu) {
 #pragma unroll
-        for (int i = 0; i < kV; ++i) out[i] = silu2<kFast>(out[i]);
+        for (int i = 0; i < kV; ++i) out[i] = silu2(out[i]);
     }
     float y0[kV], y1[kV];
 #pragma unroll
@@ -335,7 +313,6 @@ __device__ __forceinline__ void trim(Vec8<T> &v, const Span &s, int i, bool whol
 
 template <typename Tin, typename Tout, int W, bool kR>
 __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const ConvParams p, int nblk) {
-    constexpr bool kFast = sizeof(Tin) == 2;
     const int64_t L = p.L, n = p.batch * p.dim * L;
     const int64_t d = blockIdx.x / nblk;  // the blocks of a channel follow one another: one cluster
     const int rank = (int)(blockIdx.x % nblk);
@@ -453,7 +430,7 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
                 float2 pre = both(bias);
 #pragma unroll
                 for (int j = 0; j < W; ++j) pre = fma2(both(w[j]), tap[j], pre);
-                sl = conv_slope<kFast>(pre, sl);
+                sl = conv_slope(pre, sl);
             }
 #pragma unroll
             for (int j = 0; j < W; ++j) {
@@ -510,7 +487,7 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
                 if (!seen) break;
                 const float pre = silu ? conv_at<Tin, W>(p, row, t, w, bias) : 0.f;
                 const float dyt = load_elem(dy, row * L + t);
-                const float slope = silu ? conv_slope<kFast>(both(pre), both(dyt)).x : dyt;
+                const float slope = silu ? conv_slope(both(pre), both(dyt)).x : dyt;
 #pragma unroll
                 for (int j = 0; j < W; ++j)
                     if (j == k - t) acc = fmaf(w[j], slope, acc);

@@ -69,35 +69,21 @@ __device__ __forceinline__ void with_flags(bool sigmoid, bool couple, F f) {
     }
 }
 
-// a, 1 - a of two gate inputs.  Fast: e = exp(-g) with its exponent held
-// below 2^126 (a NaN passes), so 1 / (1 + e) and e / (1 + e) are both finite
-// and each has its full relative precision.
-template <bool kFast>
+// a, 1 - a of two gate inputs.  e = exp(-g) has its exponent held below
+// 2^126 (a NaN passes), so 1 / (1 + e) and e / (1 + e) are both finite, and
+// each has its full relative precision: 1 - a of a slow decay does not come
+// from a subtraction.
 __device__ __forceinline__ void gate2(float2 g, bool sigmoid, float2 &a, float2 &keep) {
     if (!sigmoid) {
         a = g;
         keep = sub2(both(1.f), g);
-    } else if constexpr (kFast) {
+    } else {
         float2 t = mul2(g, both(-kLog2e));
         asm("min.NaN.f32 %0, %1, %2;" : "=f"(t.x) : "f"(t.x), "f"(126.f));
         asm("min.NaN.f32 %0, %1, %2;" : "=f"(t.y) : "f"(t.y), "f"(126.f));
         const float2 e = make_float2(sfu_exp2(t.x), sfu_exp2(t.y)), u = add2(e, both(1.f));
         a = make_float2(sfu_rcp(u.x), sfu_rcp(u.y));
         keep = mul2(e, a);
-    } else {
-        sigmoid2<false>(g.x, a.x, keep.x);
-        sigmoid2<false>(g.y, a.y, keep.y);
-    }
-}
-
-// z sigmoid(z).
-template <bool kFast>
-__device__ __forceinline__ float2 gated2(float2 z) {
-    if constexpr (kFast) {
-        const float2 t = mul2(z, both(-kLog2e)), u = add2(make_float2(sfu_exp2(t.x), sfu_exp2(t.y)), both(1.f));
-        return mul2(z, make_float2(sfu_rcp(u.x), sfu_rcp(u.y)));
-    } else {
-        return make_float2(z.x / (1.f + expf(-z.x)), z.y / (1.f + expf(-z.y)));
     }
 }
 
@@ -180,7 +166,6 @@ __device__ __forceinline__ void bounds_of(const Row &r, int64_t v, int &lo, int 
 // `lanes`) have a row of their own.
 template <typename Tin, typename Tout, bool kZ, bool kR, bool kShared, int kG>
 __global__ void __launch_bounds__(512) glr_fwd_kernel(const GlrParams p, int lanes) {
-    constexpr bool kFast = sizeof(Tin) == 2;
     constexpr int kVecs = kGlrVecs<Tin>, kE = kVecs * kV;  // steps of a lane
     __shared__ Pair pairs[2][kMaxWarps];
     const int G = kG ? kG : lanes, lane = threadIdx.x & 31, in = lane & (G - 1);
@@ -210,9 +195,10 @@ __global__ void __launch_bounds__(512) glr_fwd_kernel(const GlrParams p, int lan
             for (int k = 0; k < kVecs; ++k) {
                 int lo, hi;
                 bounds_of(r, v + k * kV, lo, hi);
-                load8(ng[k], g, v + k * kV, lo, hi, vec);
-                load8(nx[k], x, v + k * kV, lo, hi, vec);
-                if constexpr (kZ) load8(nz[k], z, v + k * kV, lo, hi, vec);
+                const int64_t e = v + k * kV, n = p.rows * p.L - r.base;  // (elements from r.base to the tensor's end)
+                load_row8(ng[k], g, e, n, lo, hi, vec);
+                load_row8(nx[k], x, e, n, lo, hi, vec);
+                if constexpr (kZ) load_row8(nz[k], z, e, n, lo, hi, vec);
                 if constexpr (kR) ncut |= start_bits(p.reset, bl + v + k * kV, bl_all, lo, hi) << (k * kV);
             }
         }
@@ -230,7 +216,7 @@ __global__ void __launch_bounds__(512) glr_fwd_kernel(const GlrParams p, int lan
 #pragma unroll
             for (int i = 0; i < kE; i += 2) {
                 float2 a2, k2, b2 = nx[i / kV].pair(i % kV / 2);
-                gate2<kFast>(ng[i / kV].pair(i % kV / 2), sig.value, a2, k2);
+                gate2(ng[i / kV].pair(i % kV / 2), sig.value, a2, k2);
                 if (cpl.value) b2 = mul2(k2, b2);
                 a[i] = a2.x, a[i + 1] = a2.y, b[i] = b2.x, b[i + 1] = b2.y;
             }
@@ -297,7 +283,7 @@ __global__ void __launch_bounds__(512) glr_fwd_kernel(const GlrParams p, int lan
 #pragma unroll
             for (int i = 0; i < kV; i += 2) {
                 float2 h2 = make_float2(b[k * kV + i], b[k * kV + i + 1]);
-                if constexpr (kZ) h2 = mul2(h2, gated2<kFast>(cz[k].pair(i / 2)));
+                if constexpr (kZ) h2 = mul2(h2, silu2(cz[k].pair(i / 2)));
                 o[i] = h2.x, o[i + 1] = h2.y;
             }
             if (inner && vec) {
@@ -314,7 +300,6 @@ __global__ void __launch_bounds__(512) glr_fwd_kernel(const GlrParams p, int lan
 
 template <typename Tin, typename Tout, bool kZ, bool kR, bool kShared, int kG>
 __global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p, int lanes) {
-    constexpr bool kFast = sizeof(Tin) == 2;
     __shared__ Pair pairs[2][kMaxWarps];
     const int G = kG ? kG : lanes, lane = threadIdx.x & 31, in = lane & (G - 1);
     const int W = kShared ? (int)blockDim.x >> 5 : 1, w = kShared ? (int)threadIdx.x >> 5 : 0;
@@ -343,10 +328,11 @@ __global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p, int lan
         } else {
             int lo, hi;
             bounds_of(r, v, lo, hi);
-            load8(ng, g, v, lo, hi, vec);
-            load8(nx, x, v, lo, hi, vec);
-            load8(nd, dy, v, lo, hi, vec);
-            if constexpr (kZ) load8(nz, z, v, lo, hi, vec);
+            const int64_t n = p.rows * p.L - r.base;  // elements from r.base to the tensor's end
+            load_row8(ng, g, v, n, lo, hi, vec);
+            load_row8(nx, x, v, n, lo, hi, vec);
+            load_row8(nd, dy, v, n, lo, hi, vec);
+            if constexpr (kZ) load_row8(nz, z, v, n, lo, hi, vec);
             if constexpr (kR) ncut = start_bits(p.reset, bl + v, bl_all, lo, hi);
         }
         nin = start < r.steps ? __ldg(ckpt + start / kPiece) : 0.f;
@@ -362,10 +348,10 @@ __global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p, int lan
         float2 a[kV / 2], keep[kV / 2];
         if (sigmoid) {
 #pragma unroll
-            for (int i = 0; i < kV / 2; ++i) gate2<kFast>(ng.pair(i), true, a[i], keep[i]);
+            for (int i = 0; i < kV / 2; ++i) gate2(ng.pair(i), true, a[i], keep[i]);
         } else {
 #pragma unroll
-            for (int i = 0; i < kV / 2; ++i) gate2<kFast>(ng.pair(i), false, a[i], keep[i]);
+            for (int i = 0; i < kV / 2; ++i) gate2(ng.pair(i), false, a[i], keep[i]);
         }
         if (!inner) {
             int lo, hi;
@@ -383,18 +369,11 @@ __global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p, int lan
             xv[i] = b[i] = nx.pair(i);
             dh[i] = nd.pair(i);
             if constexpr (kZ) {
-                // dy silu(z) and dy silu'(z) = dy s (1 + z (1 - s))
+                // dy silu(z) and dy silu'(z)
                 const float2 zv = nz.pair(i);
-                float2 s;
-                if constexpr (kFast) {
-                    const float2 t = mul2(zv, both(-kLog2e)), u = add2(make_float2(sfu_exp2(t.x), sfu_exp2(t.y)), both(1.f));
-                    s = make_float2(sfu_rcp(u.x), sfu_rcp(u.y));
-                } else {
-                    s = make_float2(1.f / (1.f + expf(-zv.x)), 1.f / (1.f + expf(-zv.y)));
-                }
-                const float2 ds = mul2(dh[i], s);
-                dzv[i] = mul2(ds, fma2(zv, sub2(both(1.f), s), both(1.f)));
-                dh[i] = mul2(ds, zv);
+                const float2 s = sigmoid2(zv);
+                dzv[i] = mul2(dh[i], silu_slope2(zv, s));
+                dh[i] = mul2(dh[i], mul2(s, zv));
             }
         }
         if (couple) {
@@ -500,18 +479,17 @@ __global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p, int lan
 // One step: a thread per row, the state read and written in place.
 template <typename Tin, typename Tout>
 __global__ void __launch_bounds__(256) glr_step_kernel(const GlrParams p) {
-    constexpr bool kFast = sizeof(Tin) == 2;
     const int64_t row = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (row >= p.rows) return;
     float2 a2, keep2;
-    gate2<kFast>(both(load_elem(static_cast<const Tin *>(p.g), row)), p.sigmoid, a2, keep2);
+    gate2(both(load_elem(static_cast<const Tin *>(p.g), row)), p.sigmoid, a2, keep2);
     const float a = a2.x, keep = keep2.x;
     const float xv = load_elem(static_cast<const Tin *>(p.x), row);
     const float h = fmaf(a, p.last[row], p.couple ? keep * xv : xv);
     p.last[row] = h;
     float yv = h;
     if (p.z) {
-        yv *= gated2<kFast>(both(load_elem(static_cast<const Tin *>(p.z), row))).x;
+        yv *= silu2(both(load_elem(static_cast<const Tin *>(p.z), row))).x;
     }
     put(static_cast<Tout *>(p.y), row, yv);
 }
