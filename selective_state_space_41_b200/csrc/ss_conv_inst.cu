@@ -42,6 +42,11 @@ cudaError_t bwd(cudaStream_t s, ConvParams &p) {
     p.by_spans = divisor_of(spans_of(p.L));
     int nblk = 1;
     while (nblk < 8 && p.dim * nblk < (int64_t)layer_sm_count() * 8 && vecs > (int64_t)nblk * kConvBwdThreads) nblk *= 2;
+    if (nblk == 1) {
+        if (p.reset) conv_bwd_kernel<Tin, Tout, W, true><<<(unsigned)p.dim, kConvBwdThreads, 0, s>>>(p, nblk);
+        else conv_bwd_kernel<Tin, Tout, W, false><<<(unsigned)p.dim, kConvBwdThreads, 0, s>>>(p, nblk);
+        return cudaGetLastError();
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(p.dim * nblk));
     cfg.blockDim = dim3(kConvBwdThreads);

@@ -1375,6 +1375,10 @@ bool norm_vec(const ss_desc *desc, std::initializer_list<const void *> tensors, 
 
 template <typename K>
 cudaError_t launch_cluster(K kernel, int64_t grid, int threads, int nblk, cudaStream_t s, const NormParams &p) {
+    if (nblk == 1) {
+        kernel<<<(unsigned)grid, (unsigned)threads, 0, s>>>(p, nblk);
+        return cudaGetLastError();
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3((unsigned)threads);

@@ -112,10 +112,10 @@ def _out_type(dtype, x, name):
 
 
 def _new(x, dtype=None):
-    """A dense tensor of x's shape."""
+    """A dense tensor of x's shape on its device."""
     if (dtype is None or dtype is x.dtype) and x.is_contiguous():
         return torch.empty_like(x)
-    return torch.empty(x.shape, dtype=dtype or x.dtype, device=x.device)
+    return x.new_empty(x.shape, dtype=dtype or x.dtype)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -166,8 +166,8 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, rms=False, return_stats=
     mean = rstd = None
     if return_stats:
         kept = x.shape[:1] + x.shape[2:]
-        rstd = torch.empty(kept, dtype=_F32, device=x.device)
-        mean = None if rms else torch.empty(kept, dtype=_F32, device=x.device)
+        rstd = x.new_empty(kept, dtype=_F32)
+        mean = None if rms else x.new_empty(kept, dtype=_F32)
     _norm_fwd(x, y, weight, bias, eps, rms, mean, rstd)
     return (y, mean, rstd) if return_stats else y
 
@@ -177,6 +177,23 @@ def ss_norm_bwd_workspace_bytes(batch, dim, seqlen, in_dtype=torch.bfloat16, out
     return int(lib().ss_norm_bwd_workspace_bytes(ctypes.byref(desc)))
 
 
+def _norm_bwd(x, dy, rstd, dx, mean, weight, dweight, dbias, workspace):
+    batch, dim, L = _norm_sizes(x)
+    kept = x.shape[:1] + x.shape[2:]
+    dy = _input(dy, "dy", x.shape, _out_type(dy.dtype, x, "dy"), x)
+    mean, rstd = _input(mean, "mean", kept, _F32, x), _input(rstd, "rstd", kept, _F32, x)
+    weight = _input(weight, "weight", (dim,), _F32, x)
+    desc, size = _desc(batch, dim, L, x, dy.dtype), 0
+    if workspace is not None:
+        size = workspace.numel() * workspace.element_size()
+    elif dweight is not None or dbias is not None:
+        size = lib().ss_norm_bwd_workspace_bytes(desc)
+        workspace = x.new_empty(size, dtype=torch.uint8)
+    _check(lib().ss_norm_bwd(desc, x.data_ptr(), _p(weight), _p(mean), rstd.data_ptr(), dy.data_ptr(),
+                             dx.data_ptr(), _p(dweight), _p(dbias), _p(workspace), size, _stream(x)),
+           "ss_norm_bwd")
+
+
 @_on_device
 def ss_norm_bwd(x, dy, rstd, dx, mean=None, weight=None, dweight=None, dbias=None, workspace=None):
     """Queue the norm's backward from the forward's mean and rstd (mean None:
@@ -184,21 +201,9 @@ def ss_norm_bwd(x, dy, rstd, dx, mean=None, weight=None, dweight=None, dbias=Non
     ``workspace``: a CUDA tensor of ss_norm_bwd_workspace_bytes() bytes, made
     here when None and needed."""
     x = _main(x, (2, 3), "x")
-    batch, dim, L = _norm_sizes(x)
-    kept = x.shape[:1] + x.shape[2:]
-    dy = _input(dy, "dy", x.shape, _out_type(dy.dtype, x, "dy"), x)
-    mean, rstd = _input(mean, "mean", kept, _F32, x), _input(rstd, "rstd", kept, _F32, x)
-    weight = _input(weight, "weight", (dim,), _F32, x)
     _output(dx, "dx", x.shape, x.dtype, x)
-    _output(dweight, "dweight", (dim,), _F32, x), _output(dbias, "dbias", (dim,), _F32, x)
-    desc = _desc(batch, dim, L, x, dy.dtype)
-    if workspace is None and (dweight is not None or dbias is not None):
-        n = lib().ss_norm_bwd_workspace_bytes(desc)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
-    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().ss_norm_bwd(desc, x.data_ptr(), _p(weight), _p(mean), rstd.data_ptr(), dy.data_ptr(),
-                             dx.data_ptr(), _p(dweight), _p(dbias), _p(workspace), size, _stream(x)),
-           "ss_norm_bwd")
+    _output(dweight, "dweight", x.shape[1:2], _F32, x), _output(dbias, "dbias", x.shape[1:2], _F32, x)
+    _norm_bwd(x, dy, rstd, dx, mean, weight, dweight, dbias, workspace)
 
 
 @_on_device
@@ -208,11 +213,12 @@ def layer_norm_bwd(x, dy, rstd, mean=None, weight=None, bias=None, rms=False):
     (``return_stats``); ``rms`` as there."""
     if (mean is None) != bool(rms):
         raise ValueError("mean goes with the layer norm, none with rms")
-    dim, dev = x.shape[1], x.device
-    g = {"dx": _new(x),
-         "dweight": torch.empty(dim, dtype=_F32, device=dev) if weight is not None else None,
-         "dbias": torch.empty(dim, dtype=_F32, device=dev) if bias is not None else None}
-    ss_norm_bwd(x, dy, rstd, g["dx"], mean, weight, g["dweight"], g["dbias"])
+    x = _main(x, (2, 3), "x")
+    bias = _input(bias, "bias", x.shape[1:2], _F32, x)
+    weight = _input(weight, "weight", x.shape[1:2], _F32, x)
+    g = {"dx": torch.empty_like(x), "dweight": torch.empty_like(weight) if weight is not None else None,
+         "dbias": torch.empty_like(bias) if bias is not None else None}
+    _norm_bwd(x, dy, rstd, g["dx"], mean, weight, g["dweight"], g["dbias"], None)
     return g
 
 
@@ -281,9 +287,22 @@ def causal_conv_fwd(x, weight, bias=None, silu=False, initial_state=None, reset=
     y = _new(x, out_dtype and _out_type(out_dtype, x, "out_dtype"))
     last = None
     if return_last_state:
-        last = torch.empty((*x.shape[:2], _width(weight) - 1), dtype=x.dtype, device=x.device)
+        last = x.new_empty((*x.shape[:2], _width(weight) - 1))
     _conv_fwd(x, weight, y, bias, silu, initial_state, reset, last)
     return (y, last) if return_last_state else y
+
+
+def _conv_bwd(x, weight, dy, dx, bias, silu, initial_state, reset, d_last_state, dweight, dbias, dinitial_state):
+    (batch, dim, L), W = x.shape, _width(weight)
+    state = (batch, dim, W - 1)
+    weight, bias = _input(weight, "weight", (dim, W), _F32, x), _input(bias, "bias", (dim,), _F32, x)
+    initial_state, reset = _input(initial_state, "initial_state", state, x.dtype, x), _starts(reset, batch, L, x)
+    dy = _input(dy, "dy", x.shape, _out_type(dy.dtype, x, "dy"), x)
+    d_last_state = _input(d_last_state, "d_last_state", state, x.dtype, x)
+    _check(lib().ss_conv_bwd(_desc(batch, dim, L, x, dy.dtype), W, x.data_ptr(), weight.data_ptr(), _p(bias),
+                             1 if silu else 0, _p(initial_state), _p(reset), dy.data_ptr(), _p(d_last_state),
+                             dx.data_ptr(), _p(dweight), _p(dbias), _p(dinitial_state), _stream(x)),
+           "ss_conv_bwd")
 
 
 @_on_device
@@ -293,17 +312,9 @@ def ss_conv_bwd(x, weight, dy, dx, bias=None, silu=False, initial_state=None, re
     ((dim, width) float32), dbias ((dim,) float32) and dinitial_state."""
     x = _main(x, (3,), "x")
     (batch, dim, L), W = x.shape, _width(weight)
-    state = (batch, dim, W - 1)
-    weight, bias = _input(weight, "weight", (dim, W), _F32, x), _input(bias, "bias", (dim,), _F32, x)
-    initial_state, reset = _input(initial_state, "initial_state", state, x.dtype, x), _starts(reset, batch, L, x)
-    dy = _input(dy, "dy", x.shape, _out_type(dy.dtype, x, "dy"), x)
-    d_last_state = _input(d_last_state, "d_last_state", state, x.dtype, x)
-    _output(dx, "dx", x.shape, x.dtype, x), _output(dinitial_state, "dinitial_state", state, x.dtype, x)
+    _output(dx, "dx", x.shape, x.dtype, x), _output(dinitial_state, "dinitial_state", (batch, dim, W - 1), x.dtype, x)
     _output(dweight, "dweight", (dim, W), _F32, x), _output(dbias, "dbias", (dim,), _F32, x)
-    _check(lib().ss_conv_bwd(_desc(batch, dim, L, x, dy.dtype), W, x.data_ptr(), weight.data_ptr(), _p(bias),
-                             1 if silu else 0, _p(initial_state), _p(reset), dy.data_ptr(), _p(d_last_state),
-                             dx.data_ptr(), _p(dweight), _p(dbias), _p(dinitial_state), _stream(x)),
-           "ss_conv_bwd")
+    _conv_bwd(x, weight, dy, dx, bias, silu, initial_state, reset, d_last_state, dweight, dbias, dinitial_state)
 
 
 @_on_device
@@ -311,14 +322,15 @@ def causal_conv_bwd(x, weight, dy, bias=None, silu=False, initial_state=None, re
     """Gradients of sum(dy * y) (+ sum(d_last_state * last state)) as a dict:
     dx, dweight, dbias (None without bias), dinitial_state (None without an
     initial state)."""
-    dev = x.device
-    g = {"dx": _new(x),
-         "dweight": torch.empty(weight.shape, dtype=_F32, device=dev),
-         "dbias": torch.empty(x.shape[1], dtype=_F32, device=dev) if bias is not None else None,
-         "dinitial_state": torch.empty(initial_state.shape, dtype=x.dtype, device=dev)
-         if initial_state is not None else None}
-    ss_conv_bwd(x, weight, dy, g["dx"], bias, silu, initial_state, reset, d_last_state, g["dweight"],
-                g["dbias"], g["dinitial_state"])
+    x = _main(x, (3,), "x")
+    dim, W = x.shape[1], _width(weight)
+    weight, bias = _input(weight, "weight", (dim, W), _F32, x), _input(bias, "bias", (dim,), _F32, x)
+    initial_state = _input(initial_state, "initial_state", (x.shape[0], dim, W - 1), x.dtype, x)
+    g = {"dx": torch.empty_like(x), "dweight": torch.empty_like(weight),
+         "dbias": torch.empty_like(bias) if bias is not None else None,
+         "dinitial_state": torch.empty_like(initial_state) if initial_state is not None else None}
+    _conv_bwd(x, weight, dy, g["dx"], bias, silu, initial_state, reset, d_last_state, g["dweight"], g["dbias"],
+              g["dinitial_state"])
     return g
 
 
@@ -382,6 +394,15 @@ def ss_glr_ckpt_elems(batch, dim, seqlen, in_dtype=torch.bfloat16, out_dtype=Non
     return int(lib().ss_glr_ckpt_elems(ctypes.byref(desc)))
 
 
+def _glr_fwd(x, g, y, z, gate_sigmoid, couple, initial_state, reset, last_state, ckpt, desc):
+    batch, dim, L = x.shape
+    g, z = _input(g, "g", x.shape, x.dtype, x), _input(z, "z", x.shape, x.dtype, x)
+    initial_state = _input(initial_state, "initial_state", (batch, dim), _F32, x)
+    reset = _starts(reset, batch, L, x)
+    _check(lib().ss_glr_fwd(desc, x.data_ptr(), g.data_ptr(), _p(z), 1 if gate_sigmoid else 0, 1 if couple else 0,
+                            _p(initial_state), _p(reset), _p(y), _p(last_state), _p(ckpt), _stream(x)), "ss_glr_fwd")
+
+
 @_on_device
 def ss_glr_fwd(x, g, y, z=None, gate_sigmoid=True, couple=False, initial_state=None, reset=None, last_state=None,
                ckpt=None):
@@ -391,17 +412,12 @@ def ss_glr_fwd(x, g, y, z=None, gate_sigmoid=True, couple=False, initial_state=N
     nonzero where a sequence starts; ckpt: ss_glr_ckpt_elems() float32, for
     the backward."""
     x = _main(x, (3,), "x")
-    batch, dim, L = x.shape
-    g, z = _input(g, "g", x.shape, x.dtype, x), _input(z, "z", x.shape, x.dtype, x)
     out = x.dtype if y is None else _out_type(y.dtype, x, "y")
-    _output(y, "y", x.shape, out, x), _output(last_state, "last_state", (batch, dim), _F32, x)
-    initial_state = _input(initial_state, "initial_state", (batch, dim), _F32, x)
-    reset, desc = _starts(reset, batch, L, x), _desc(batch, dim, L, x, out)
+    _output(y, "y", x.shape, out, x), _output(last_state, "last_state", x.shape[:2], _F32, x)
+    desc = _desc(*x.shape, x, out)
     if ckpt is not None:
         _output(ckpt, "ckpt", (int(lib().ss_glr_ckpt_elems(desc)),), _F32, x)
-    _check(lib().ss_glr_fwd(desc, x.data_ptr(), g.data_ptr(), _p(z), 1 if gate_sigmoid else 0,
-                            1 if couple else 0, _p(initial_state), _p(reset), _p(y), _p(last_state), _p(ckpt),
-                            _stream(x)), "ss_glr_fwd")
+    _glr_fwd(x, g, y, z, gate_sigmoid, couple, initial_state, reset, last_state, ckpt, desc)
 
 
 @_on_device
@@ -409,16 +425,26 @@ def gated_recurrence_fwd(x, g, z=None, gate_sigmoid=True, couple=False, initial_
                          return_last_state=False, return_ckpt=False, out_dtype=None):
     """y of the gated linear recurrence, then the last state
     (``return_last_state``) and the backward's checkpoints (``return_ckpt``)."""
-    out = out_dtype or x.dtype
-    y = _new(x, out)
-    last = torch.empty(x.shape[:2], dtype=_F32, device=x.device) if return_last_state else None
-    ckpt = None
-    if return_ckpt:
-        n = lib().ss_glr_ckpt_elems(_desc(*x.shape, x, _out_type(out, x, "out_dtype")))
-        ckpt = torch.empty(n, dtype=_F32, device=x.device)
-    ss_glr_fwd(x, g, y, z, gate_sigmoid, couple, initial_state, reset, last, ckpt)
+    x = _main(x, (3,), "x")
+    out = _out_type(out_dtype or x.dtype, x, "out_dtype")
+    y, desc = _new(x, out), _desc(*x.shape, x, out)
+    last = x.new_empty(x.shape[:2], dtype=_F32) if return_last_state else None
+    ckpt = x.new_empty(lib().ss_glr_ckpt_elems(desc), dtype=_F32) if return_ckpt else None
+    _glr_fwd(x, g, y, z, gate_sigmoid, couple, initial_state, reset, last, ckpt, desc)
     more = ((last,) if return_last_state else ()) + ((ckpt,) if return_ckpt else ())
     return (y, *more) if more else y
+
+
+def _glr_bwd(x, g, dy, ckpt, dx, dg, z, dz, gate_sigmoid, couple, reset, d_last_state, dinitial_state):
+    batch, dim, L = x.shape
+    g, z = _input(g, "g", x.shape, x.dtype, x), _input(z, "z", x.shape, x.dtype, x)
+    dy = _input(dy, "dy", x.shape, _out_type(dy.dtype, x, "dy"), x)
+    desc, reset = _desc(batch, dim, L, x, dy.dtype), _starts(reset, batch, L, x)
+    ckpt = _input(ckpt, "ckpt", (lib().ss_glr_ckpt_elems(desc),), _F32, x)
+    d_last_state = _input(d_last_state, "d_last_state", (batch, dim), _F32, x)
+    _check(lib().ss_glr_bwd(desc, x.data_ptr(), g.data_ptr(), _p(z), 1 if gate_sigmoid else 0, 1 if couple else 0,
+                            _p(reset), ckpt.data_ptr(), dy.data_ptr(), _p(d_last_state), dx.data_ptr(),
+                            dg.data_ptr(), _p(dz), _p(dinitial_state), _stream(x)), "ss_glr_bwd")
 
 
 @_on_device
@@ -427,17 +453,9 @@ def ss_glr_bwd(x, g, dy, ckpt, dx, dg, z=None, dz=None, gate_sigmoid=True, coupl
     """Queue the recurrence's backward, from the forward's checkpoints, into
     dx, dg, dz (with z) and, where given, dinitial_state."""
     x = _main(x, (3,), "x")
-    batch, dim, L = x.shape
-    g, z = _input(g, "g", x.shape, x.dtype, x), _input(z, "z", x.shape, x.dtype, x)
-    dy = _input(dy, "dy", x.shape, _out_type(dy.dtype, x, "dy"), x)
-    desc, reset = _desc(batch, dim, L, x, dy.dtype), _starts(reset, batch, L, x)
-    ckpt = _input(ckpt, "ckpt", (int(lib().ss_glr_ckpt_elems(desc)),), _F32, x)
-    d_last_state = _input(d_last_state, "d_last_state", (batch, dim), _F32, x)
     _output(dx, "dx", x.shape, x.dtype, x), _output(dg, "dg", x.shape, x.dtype, x)
-    _output(dz, "dz", x.shape, x.dtype, x), _output(dinitial_state, "dinitial_state", (batch, dim), _F32, x)
-    _check(lib().ss_glr_bwd(desc, x.data_ptr(), g.data_ptr(), _p(z), 1 if gate_sigmoid else 0,
-                            1 if couple else 0, _p(reset), ckpt.data_ptr(), dy.data_ptr(), _p(d_last_state),
-                            dx.data_ptr(), dg.data_ptr(), _p(dz), _p(dinitial_state), _stream(x)), "ss_glr_bwd")
+    _output(dz, "dz", x.shape, x.dtype, x), _output(dinitial_state, "dinitial_state", x.shape[:2], _F32, x)
+    _glr_bwd(x, g, dy, ckpt, dx, dg, z, dz, gate_sigmoid, couple, reset, d_last_state, dinitial_state)
 
 
 @_on_device
@@ -446,13 +464,11 @@ def gated_recurrence_bwd(x, g, dy, ckpt, z=None, gate_sigmoid=True, couple=False
     """Gradients of sum(dy * y) (+ sum(d_last_state * last state)) as a dict:
     dx, dg, dz (None without z), dinitial_state (None unless asked for).
     ckpt: gated_recurrence_fwd's, of the same inputs, initial state and starts."""
-    dev = x.device
-    d = {"dx": _new(x),
-         "dg": _new(x),
-         "dz": _new(x) if z is not None else None,
-         "dinitial_state": torch.empty(x.shape[:2], dtype=_F32, device=dev) if return_dinitial_state else None}
-    ss_glr_bwd(x, g, dy, ckpt, d["dx"], d["dg"], z, d["dz"], gate_sigmoid, couple, reset, d_last_state,
-               d["dinitial_state"])
+    x = _main(x, (3,), "x")
+    d = {"dx": torch.empty_like(x), "dg": torch.empty_like(x), "dz": torch.empty_like(x) if z is not None else None,
+         "dinitial_state": x.new_empty(x.shape[:2], dtype=_F32) if return_dinitial_state else None}
+    _glr_bwd(x, g, dy, ckpt, d["dx"], d["dg"], z, d["dz"], gate_sigmoid, couple, reset, d_last_state,
+             d["dinitial_state"])
     return d
 
 
