@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(const ConvParams p) {
     }
 }
 
-constexpr int kConvBwdThreads = 128;
+constexpr int kConvBwdThreads = 128;  // of a block, at most: fewer where a channel has fewer spans
 
 // The backward's next spans, copied in while the present ones are worked on:
 // a slot for each thread's 16 elements of a tensor, and one on either side.
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
             }
         }
         if (t == 0) xs[buf].fill(1, x, s.e - kV, n, s.lo(-kV), s.hi(-kV), vec);
-        if (t == kConvBwdThreads - 1) {
+        if (t == (int)blockDim.x - 1) {
             xs[buf].fill(2 * t + 4, x, s.e + kSpan, n, s.lo(kSpan), s.hi(kSpan), vec);
             gs[buf].fill(2 * t + 4, dy, s.e + kSpan, n, s.lo(kSpan), s.hi(kSpan), vec);
         }
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
             m = span_starts(p, b, s, 0) | span_starts(p, b, s, kV) << kV;
             starts[t + 1] = m;
             if (t == 0) starts[0] = span_starts(p, b, s, -kV) << kV;
-            if (t == kConvBwdThreads - 1) starts[t + 2] = span_starts(p, b, s, kSpan);
+            if (t == (int)blockDim.x - 1) starts[t + 2] = span_starts(p, b, s, kSpan);
         }
         __syncthreads();
         if constexpr (kR) {
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
     __syncthreads();
     if (threadIdx.x <= W) {
         float s = 0.f;
-        for (int k = 0; k < kConvBwdThreads / 32; ++k) s += part[k][threadIdx.x];
+        for (int k = 0; k < (int)blockDim.x / 32; ++k) s += part[k][threadIdx.x];
         mine[threadIdx.x] = s;
     }
     if (nblk > 1) {

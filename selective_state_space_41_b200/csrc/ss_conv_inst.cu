@@ -43,8 +43,9 @@ cudaError_t bwd(cudaStream_t s, ConvParams &p) {
     int nblk = 1;
     while (nblk < 8 && p.dim * nblk < (int64_t)layer_sm_count() * 8 && vecs > (int64_t)nblk * kConvBwdThreads) nblk *= 2;
     if (nblk == 1) {
-        if (p.reset) conv_bwd_kernel<Tin, Tout, W, true><<<(unsigned)p.dim, kConvBwdThreads, 0, s>>>(p, nblk);
-        else conv_bwd_kernel<Tin, Tout, W, false><<<(unsigned)p.dim, kConvBwdThreads, 0, s>>>(p, nblk);
+        const int threads = vecs < kConvBwdThreads ? (int)(vecs + 31) / 32 * 32 : kConvBwdThreads;
+        if (p.reset) conv_bwd_kernel<Tin, Tout, W, true><<<(unsigned)p.dim, threads, 0, s>>>(p, nblk);
+        else conv_bwd_kernel<Tin, Tout, W, false><<<(unsigned)p.dim, threads, 0, s>>>(p, nblk);
         return cudaGetLastError();
     }
     cudaLaunchConfig_t cfg{};
