@@ -302,13 +302,12 @@ struct Slots {
     }
 };
 
-// Clears what of a vector is not in the row (it was not copied, or belongs to
-// a neighbouring row): all of it or nothing where rows are whole vectors.
+// Clears what of the vector at step t0 + i is not in the row.
 template <typename T>
-__device__ __forceinline__ void trim(Vec8<T> &v, const Span &s, int i, bool whole_rows) {
+__device__ __forceinline__ void trim(Vec8<T> &v, const Span &s, int i) {
     const int lo = s.lo(i), hi = s.hi(i);
     if (hi <= lo) v.clear();
-    else if (!whole_rows && (lo > 0 || hi < kV)) v.keep(lo, hi);
+    else if (lo > 0 || hi < kV) v.keep(lo, hi);
 }
 
 template <typename Tin, typename Tout, int W, bool kR>
@@ -354,8 +353,8 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
                 gs[buf].fill(2 * t + 2 + i, dy, s.e + i * kV, n, s.lo(i * kV), s.hi(i * kV), vec);
             }
         }
-        if (t == 0) xs[buf].fill(1, x, s.e - kV, n, s.lo(-kV), s.hi(-kV), vec);
-        if (t == (int)blockDim.x - 1) {
+        if (t == 0 && s.head > 0) xs[buf].fill(1, x, s.e - kV, n, s.lo(-kV), s.hi(-kV), vec);
+        if (t == (int)blockDim.x - 1 && s.tail > kSpan) {
             xs[buf].fill(2 * t + 4, x, s.e + kSpan, n, s.lo(kSpan), s.hi(kSpan), vec);
             gs[buf].fill(2 * t + 4, dy, s.e + kSpan, n, s.lo(kSpan), s.hi(kSpan), vec);
         }
@@ -402,11 +401,17 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
             for (int i = 0; i < 4; ++i) xs[buf].read(v[i], 2 * t + 1 + i);
 #pragma unroll
             for (int i = 0; i < 3; ++i) gs[buf].read(u[i], 2 * t + 2 + i);
-            if (s.head < kV || s.tail < kSpan + kV) {
+            // what is not in the row: it was not copied, or belongs to a neighbouring one
+            if (whole_rows) {
+                if (s.head <= 0) v[0].clear();
+                if (s.tail <= 0) v[1].clear(), u[0].clear();  // (a thread without a span)
+                if (s.tail <= kV) v[2].clear(), u[1].clear();
+                if (s.tail <= kSpan) v[3].clear(), u[2].clear();
+            } else if (s.head < kV || s.tail < kSpan + kV) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) trim(v[i], s, (i - 1) * kV, whole_rows);
+                for (int i = 0; i < 4; ++i) trim(v[i], s, (i - 1) * kV);
 #pragma unroll
-                for (int i = 0; i < 3; ++i) trim(u[i], s, i * kV, whole_rows);
+                for (int i = 0; i < 3; ++i) trim(u[i], s, i * kV);
             }
             win.take(p, v, s, row);
             // outputs outside the row have dy = 0, and with it no part in anything
