@@ -1001,7 +1001,8 @@ __global__ void __launch_bounds__(32 * kTileWarps, 2) norm_tile_fwd_kernel(const
         __syncthreads();
         if (t < G::kSteps) {
             const float2 all = join(&part[0][t], G::kSteps, warps, channels);
-            const float rstd = rsqrtf(fmaf(fmaxf(all.y, 0.f), p.inv_dim, p.eps));
+            const float S2 = all.y < 0.f ? 0.f : all.y;  // (a NaN passes)
+            const float rstd = rsqrtf(fmaf(S2, p.inv_dim, p.eps));
             stat[0][t] = -all.x, stat[1][t] = rstd;
             const int64_t s = tile * G::kSteps + t;
             if (s < p.batch * p.L) {

@@ -176,3 +176,26 @@ def test_autograd(shape, rms):
     x.grad = None
     ss.layer_norm_fn(x, w, b, rms=rms).sum().backward()
     assert torch.isfinite(x.grad).all()
+
+
+# rows, wide rows, tiles of whole vectors, clusters, wide steps
+KINDS = [(4, 96, 1), (2, 17000, 1), (2, 96, 40), (2, 1536, 40), (2, 96, 37), (2, 1536, 37), (1, 33000, 24)]
+
+
+@pytest.mark.parametrize("shape", KINDS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rms", [False, True])
+def test_nonfinite_reaches_its_whole_step(shape, dtype, rms):
+    """One channel's NaN or infinity, as the formula has it: NaN in every
+    channel of the step (rms: zero beside an infinity)."""
+    x = rand(*shape, seed=31, dtype=dtype)
+    last = x.shape[2] - 1
+    x[0, 5, 0], x[1 % x.shape[0], 90, last] = float("nan"), float("inf")
+    y, mean, rstd = ss.layer_norm_fwd(x.cuda(), rms=rms, return_stats=True)
+    c = x.double() if rms else x.double() - x.double().mean(1, keepdim=True)
+    want_r = (c.square().mean(1, keepdim=True) + 1e-5).rsqrt()
+    want = c * want_r
+    assert torch.equal(y.isnan().cpu(), want.isnan())
+    assert torch.equal(rstd.isnan().cpu(), want_r[:, 0].isnan())
+    assert torch.equal(rstd.cpu() == 0, want_r[:, 0] == 0)
+    assert torch.equal(y.isfinite().cpu(), want.isfinite())
