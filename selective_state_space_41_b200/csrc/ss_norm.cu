@@ -1292,6 +1292,15 @@ struct NormPlan {
 constexpr int kRowThreads = 256;          // of a block, unless one row takes more
 constexpr int64_t kSmMost = 228 * 1024;   // shared memory of an SM, and of a block with its reserve of 1 KB
 constexpr int64_t kBlockMost = 227 * 1024;
+constexpr int64_t kTileOwn = 5 * 1024;    // the tile kernels' static shared memory, rounded up
+constexpr int kSmDefault = 40 * 1024;     // dynamic shared memory that needs no attribute beside a kernel's own
+
+// The most dynamic shared memory that any launch of the kernel asks for: one
+// value for all of them, as calls from other threads set it too.
+template <typename K>
+cudaError_t allow_smem(K kernel, int most) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
 
 // Dynamic shared memory of the tile kernels.
 int64_t tile_smem(int64_t dim, const NormPlan &pl, bool back) {
@@ -1330,7 +1339,7 @@ NormPlan norm_plan(const ss_desc *desc, bool vec, bool back) {
     const int64_t steps = desc->in_dtype == SS_BF16 ? 32 : 16, tiles = (n + steps - 1) / steps;
     pl.batches = (int)((desc->dim + 511) / 512);
     pl.T = (int)(((desc->dim + pl.batches - 1) / pl.batches + 31) / 32 * 32);
-    const int64_t smem = tile_smem(desc->dim, pl, back) + 5 * 1024;  // and the kernel's own
+    const int64_t smem = tile_smem(desc->dim, pl, back) + kTileOwn;
     if (vec && smem <= kBlockMost && !(back && desc->in_dtype != desc->out_dtype) && desc->seqlen <= 1 << 20) {
         pl.kind = kTile;
         int64_t resident = 65536 / (pl.T * (back ? 128 : 64));
@@ -1398,9 +1407,8 @@ cudaError_t launch_rows(bool back, const NormPlan &pl, cudaStream_t s, const Nor
     const int threads = pl.T * pl.per;
     if (back) {
         const size_t smem = pl.per > 1 ? (size_t)pl.per * p.dim * 2 * sizeof(float) : 0;  // 48 KB at most: 256 threads of 24 columns
-        if (smem > 40 * 1024) {  // more than the default leaves beside the kernel's own
-            const cudaError_t e = cudaFuncSetAttribute(norm_rows_bwd_kernel<Tin, Tout, kNv, kVec>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (smem > kSmDefault) {
+            const cudaError_t e = allow_smem(norm_rows_bwd_kernel<Tin, Tout, kNv, kVec>, 48 * 1024);
             if (e != cudaSuccess) return e;
         }
         norm_rows_bwd_kernel<Tin, Tout, kNv, kVec><<<(unsigned)pl.parts, threads, smem, s>>>(p, pl.T);
@@ -1421,8 +1429,8 @@ template <typename Tin, typename Tout>
 cudaError_t launch_tile(bool back, const NormPlan &pl, cudaStream_t s, const NormParams &p) {
     const auto kernel = back ? norm_tile_bwd_kernel<Tin> : norm_tile_fwd_kernel<Tin, Tout>;
     const int smem = (int)tile_smem(p.dim, pl, back);
-    if (smem > 40 * 1024) {  // more than the default leaves beside the kernel's own
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (smem > kSmDefault) {
+        const cudaError_t e = allow_smem(kernel, (int)(kBlockMost - kTileOwn));
         if (e != cudaSuccess) return e;
     }
     kernel<<<(unsigned)pl.blocks, pl.T, smem, s>>>(p, pl.batches);

@@ -1,5 +1,7 @@
 """Normalisation over the channels on the GPU against the 64-bit reference
 (layer_ref.py gives the values and the bounds)."""
+import threading
+
 import pytest
 import torch
 
@@ -199,3 +201,27 @@ def test_nonfinite_reaches_its_whole_step(shape, dtype, rms):
     assert torch.equal(rstd.isnan().cpu(), want_r[:, 0].isnan())
     assert torch.equal(rstd.cpu() == 0, want_r[:, 0] == 0)
     assert torch.equal(y.isfinite().cpu(), want.isfinite())
+
+
+def test_sizes_of_two_threads_do_not_meet():
+    """Calls of different widths from two threads at once: neither changes what
+    the other's launch may use."""
+    xs = [rand(1, d, 64, seed=d, dtype=BF).cuda() for d in (768, 1536)]
+    want = [ss.layer_norm_fwd(x) for x in xs]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(x, y):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(3000):
+                    got = ss.layer_norm_fwd(x)
+                torch.cuda.current_stream().synchronize()
+                assert torch.equal(got, y)
+        except Exception as e:  # noqa: BLE001 (handed to the test)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(xs, want)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not failed, failed
