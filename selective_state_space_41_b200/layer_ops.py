@@ -185,6 +185,8 @@ def _norm_bwd(x, dy, rstd, dx, mean, weight, dweight, dbias, workspace):
     weight = _input(weight, "weight", (dim,), _F32, x)
     desc, size = _desc(batch, dim, L, x, dy.dtype), 0
     if workspace is not None:
+        if workspace.get_device() != x.get_device() or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {x.device}, got one on {workspace.device}")
         size = workspace.numel() * workspace.element_size()
     elif dweight is not None or dbias is not None:
         size = lib().ss_norm_bwd_workspace_bytes(desc)

@@ -225,3 +225,16 @@ def test_sizes_of_two_threads_do_not_meet():
     [t.start() for t in threads]
     [t.join() for t in threads]
     assert not failed, failed
+
+
+def test_workspace_elsewhere_is_refused():
+    """A workspace that the kernels cannot write, or that is not one block."""
+    x = rand(4, 64, 1, seed=1).cuda()
+    dw, dx, rstd = torch.empty(64, device="cuda"), torch.empty_like(x), torch.ones(4, 1, device="cuda")
+    n = ss.ss_norm_bwd_workspace_bytes(4, 64, 1, F32)
+    for ws in (torch.empty(n, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8, device="cuda").expand(n)):
+        with pytest.raises(ValueError, match="workspace"):
+            ss.ss_norm_bwd(x, x, rstd, dx, dweight=dw, workspace=ws)
+    with pytest.raises(ss.SelscanError):
+        ss.ss_norm_bwd(x, x, rstd, dx, dweight=dw, workspace=torch.empty(n - 4, dtype=torch.uint8, device="cuda"))
+    ss.ss_norm_bwd(x, x, rstd, dx, dweight=dw, workspace=torch.empty(n, dtype=torch.uint8, device="cuda"))
