@@ -50,6 +50,7 @@ struct ConvParams {
     Divisor by_spans, by_dim;  // spans of a row, channels
     int small;            // the spans count in 31 bits (forward: of all rows; backward: of a channel)
     int64_t chunks, groups;  // forward with starts: warps of spans to a row, groups of 8 channels to an entry
+    int64_t rounds, each;    // backward: rounds of a block's threads to a channel, and to a block
 };
 
 cudaError_t conv_fwd_f32_f32(int width, cudaStream_t s, ConvParams &p);
@@ -270,11 +271,11 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(const ConvParams p) {
 constexpr int kConvBwdThreads = 128;  // of a block, at most: fewer where a channel has fewer spans
 
 // The backward's next spans, copied in while the present ones are worked on:
-// a slot for each thread's 16 elements of a tensor, and one on either side.
+// a slot for each thread's 16 elements of a tensor, and one before them.
 template <typename T>
 struct Slots {
     static constexpr int kQ = sizeof(T) / 2;  // 16-byte words of a vector
-    uint4 w[(kConvBwdThreads + 2) * 2 * kQ];
+    uint4 w[(kConvBwdThreads + 1) * 2 * kQ];
     // Both vectors of a thread whose steps all lie in the row.
     __device__ __forceinline__ void fill_whole(int t, const T *p) {
 #pragma unroll
@@ -331,8 +332,11 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
     __shared__ Slots<Tin> xs[2];
     __shared__ Slots<Tout> gs[2];
     __shared__ uint32_t starts[kR ? kConvBwdThreads + 2 : 1];
+    __shared__ float heads[2][W - 1][kConvBwdThreads];  // q of each thread's outputs 0 .. W-2
     const int t = threadIdx.x;
-    const int64_t nv = spans_of(L), total = p.batch * nv, stride = (int64_t)nblk * blockDim.x;
+    const int64_t nv = spans_of(L), total = p.batch * nv;
+    // The block's rounds of blockDim spans, worked from the last to the first.
+    const int64_t first = rank * p.each, behind = min(first + p.each, p.rounds);
     // Span q of the channel; one behind the last has no step.
     const auto place = [&](int64_t q, int64_t &b) {
         const bool there = q < total;
@@ -354,22 +358,29 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
             }
         }
         if (t == 0 && s.head > 0) xs[buf].fill(1, x, s.e - kV, n, s.lo(-kV), s.hi(-kV), vec);
-        if (t == (int)blockDim.x - 1 && s.tail > kSpan) {
-            xs[buf].fill(2 * t + 4, x, s.e + kSpan, n, s.lo(kSpan), s.hi(kSpan), vec);
-            gs[buf].fill(2 * t + 4, dy, s.e + kSpan, n, s.lo(kSpan), s.hi(kSpan), vec);
-        }
         cp_async_commit();
     };
     int buf = 0;
     int64_t b, next_b;
-    Span s, next = place((int64_t)rank * blockDim.x + t, next_b);
-    fill(next, 0);
-    for (int64_t q0 = (int64_t)rank * blockDim.x; q0 < total; q0 += stride, buf ^= 1) {
-        const int64_t q = q0 + t;
+    Span s, next = place((behind - 1) * blockDim.x + t, next_b);
+    if (first < behind) {
+        fill(next, 0);
+        // What later rounds leave for the last thread, for the first of them.
+        if (t == (int)blockDim.x - 1 && next.tail > kSpan) {
+            const int64_t row = next_b * p.dim + d;
+            for (int k = 0; k < W - 1 && k < next.tail - kSpan; ++k) {
+                const int64_t at = next.t0 + kSpan + k;
+                const float dyt = load_elem(dy, row * L + at);
+                heads[1][k][0] = silu ? conv_slope(both(conv_at<Tin, W>(p, row, at, w, bias)), both(dyt)).x : dyt;
+            }
+        }
+    }
+    for (int64_t round = behind - 1; round >= first; --round, buf ^= 1) {
+        const int64_t q = round * blockDim.x + t;
         const bool there = q < total;
         s = next, b = next_b;
-        if (q0 + stride < total) {
-            next = place(q + stride, next_b);
+        if (round > first) {
+            next = place(q - blockDim.x, next_b);
             fill(next, buf ^ 1);
             cp_async_wait_one();
         } else {
@@ -391,64 +402,78 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
         }
         const int64_t row = b * p.dim + d;
         const bool whole = vec && s.head >= 0 && s.tail >= kSpan;
-        constexpr int kOut = kV + W - 1;  // pairs of outputs: the thread's steps and W - 1 behind
-        Window<Tin, W, 3> win;
-        float2 slope[kOut];  // first dy: outputs k and k + 8
+        Window<Tin, W, 2> win;
+        float2 slope[kV];  // first dy: outputs k and k + 8
         {
-            Vec8<Tin> v[4];
-            Vec8<Tout> u[3];
+            Vec8<Tin> v[3];
+            Vec8<Tout> u[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) xs[buf].read(v[i], 2 * t + 1 + i);
+            for (int i = 0; i < 3; ++i) xs[buf].read(v[i], 2 * t + 1 + i);
 #pragma unroll
-            for (int i = 0; i < 3; ++i) gs[buf].read(u[i], 2 * t + 2 + i);
+            for (int i = 0; i < 2; ++i) gs[buf].read(u[i], 2 * t + 2 + i);
             // what is not in the row: it was not copied, or belongs to a neighbouring one
             if (whole_rows) {
                 if (s.head <= 0) v[0].clear();
                 if (s.tail <= 0) v[1].clear(), u[0].clear();  // (a thread without a span)
                 if (s.tail <= kV) v[2].clear(), u[1].clear();
-                if (s.tail <= kSpan) v[3].clear(), u[2].clear();
-            } else if (s.head < kV || s.tail < kSpan + kV) {
+            } else if (s.head < kV || s.tail < kSpan) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) trim(v[i], s, (i - 1) * kV);
+                for (int i = 0; i < 3; ++i) trim(v[i], s, (i - 1) * kV);
 #pragma unroll
-                for (int i = 0; i < 3; ++i) trim(u[i], s, i * kV);
+                for (int i = 0; i < 2; ++i) trim(u[i], s, i * kV);
             }
             win.take(p, v, s, row);
             // outputs outside the row have dy = 0, and with it no part in anything
 #pragma unroll
-            for (int k = 0; k < kOut; ++k) slope[k] = make_float2(u[k / kV][k % kV], u[k / kV + 1][k % kV]);
+            for (int k = 0; k < kV; ++k) slope[k] = make_float2(u[0][k], u[1][k]);
         }
-        __syncthreads();  // this half may be filled again
         uint32_t cut[W];
         const uint32_t slow = kR ? cuts_of<W>(m, cut) : 0u;
-        // Output by output: p, q, and what q adds to the steps of its taps and
-        // to the sums (of the thread's own outputs, k < 8).  Tap j of output k
-        // reads window position k + j, step k + j - (W-1) of the thread.
+        // Output by output: p, q, and what q adds to the sums and to the steps
+        // of its taps.  Tap j of output k reads window position k + j, step
+        // k + j - (W-1) of the thread.
         float2 g[kV];
 #pragma unroll
         for (int i = 0; i < kV; ++i) g[i] = both(0.f);
+        const auto spread = [&](int k, float2 q, auto cutting) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                const int i = k + j - (W - 1);
+                if (i >= 0 && i < kV) g[i] = fma2(both(w[j]), cutting.value ? seen(q, cut[j], k) : q, g[i]);
+            }
+        };
         const auto output = [&](int k, auto cutting) {
-            float2 tap[W], sl = slope[k];
+            float2 tap[W];
 #pragma unroll
             for (int j = 0; j < W; ++j) tap[j] = cutting.value ? seen(win.v[k + j], cut[j], k) : win.v[k + j];
             if (silu) {
                 float2 pre = both(bias);
 #pragma unroll
                 for (int j = 0; j < W; ++j) pre = fma2(both(w[j]), tap[j], pre);
-                sl = conv_slope(pre, sl);
+                slope[k] = conv_slope(pre, slope[k]);
             }
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                const int i = k + j - (W - 1);
-                if (i >= 0 && i < kV) g[i] = fma2(both(w[j]), cutting.value ? seen(sl, cut[j], k) : sl, g[i]);
-                if (k < kV) sum2[j] = fma2(sl, tap[j], sum2[j]);
-            }
-            if (k < kV) sum2[W] = add2(sum2[W], sl);
+            for (int j = 0; j < W; ++j) sum2[j] = fma2(slope[k], tap[j], sum2[j]);
+            sum2[W] = add2(sum2[W], slope[k]);
+            spread(k, slope[k], cutting);
         };
 #pragma unroll
-        for (int k = 0; k < kOut; ++k) {
+        for (int k = 0; k < kV; ++k) {
             if (kR && (slow >> k & 1u)) output(k, std::true_type{});
             else output(k, std::false_type{});
+        }
+        // The W - 1 outputs behind: the second halves' firsts, and those of the
+        // next thread, for the last one thread 0's of the round before.
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) heads[buf][k][t] = slope[k].x;
+        __syncthreads();  // (and the slots of this half may be filled again)
+        const float *next_heads = t + 1 < (int)blockDim.x ? &heads[buf][0][t + 1] : &heads[buf ^ 1][0][0];
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+            float2 q2 = make_float2(slope[k].y, next_heads[k * kConvBwdThreads]);
+            if (s.tail <= kSpan) q2.y = 0.f;
+            if (kR && (slow >> (k + kV) & 1u)) spread(k + kV, q2, std::true_type{});
+            else spread(k + kV, q2, std::false_type{});
         }
         if (p.dlast && there && s.t0 + kSpan > L - (W - 1)) {  // the last state's elements are inputs too
             bool seen = true;
@@ -482,7 +507,7 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
 
     // the state's gradient: outputs 0 .. W-2 reach it
     if (p.dh0) {
-        for (int64_t i = (int64_t)rank * blockDim.x + threadIdx.x; i < p.batch * (W - 1); i += stride) {
+        for (int64_t i = (int64_t)rank * blockDim.x + threadIdx.x; i < p.batch * (W - 1); i += (int64_t)nblk * blockDim.x) {
             const int64_t b = i / (W - 1), row = b * p.dim + d;
             const int k = (int)(i % (W - 1));  // step k - (W-1)
             float acc = 0.f;

@@ -42,8 +42,10 @@ cudaError_t bwd(cudaStream_t s, ConvParams &p) {
     p.by_spans = divisor_of(spans_of(p.L));
     int nblk = 1;
     while (nblk < 8 && p.dim * nblk < (int64_t)layer_sm_count() * 8 && vecs > (int64_t)nblk * kConvBwdThreads) nblk *= 2;
+    const int threads = vecs < kConvBwdThreads ? (int)(vecs + 31) / 32 * 32 : kConvBwdThreads;
+    p.rounds = (vecs + threads - 1) / threads;
+    p.each = (p.rounds + nblk - 1) / nblk;
     if (nblk == 1) {
-        const int threads = vecs < kConvBwdThreads ? (int)(vecs + 31) / 32 * 32 : kConvBwdThreads;
         if (p.reset) conv_bwd_kernel<Tin, Tout, W, true><<<(unsigned)p.dim, threads, 0, s>>>(p, nblk);
         else conv_bwd_kernel<Tin, Tout, W, false><<<(unsigned)p.dim, threads, 0, s>>>(p, nblk);
         return cudaGetLastError();

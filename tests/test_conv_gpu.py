@@ -164,3 +164,10 @@ def test_autograd():
     want = torch.zeros_like(x)
     want[..., -(W - 1):] = 1
     assert torch.equal(x.grad, want) and w.grad.abs().sum() == 0 and h0.grad.abs().sum() == 0
+
+
+@pytest.mark.parametrize("W,silu,every,dtype", [(2, True, 0, F32), (4, False, 40, BF), (8, True, 40, F32), (8, False, 0, BF)])
+@pytest.mark.parametrize("B,D,L", [(1, 2, 20000), (1, 3, 4133), (5, 2, 1001)])
+def test_blocks_of_a_channel(B, D, L, W, silu, every, dtype):
+    """Few channels: several blocks to each, whose parts of a row meet."""
+    run(B, D, L, W, dtype, silu=silu, every=every, seed=W)
