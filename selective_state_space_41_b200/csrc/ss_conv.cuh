@@ -14,11 +14,19 @@
 // floats: their taps are pairs too, i + j and i + j + 8.
 //
 // Forward: two bytes in and two out per bf16 element against 2 W + 5
-// operations.
+// operations.  8 x 1536 x 2048 bf16, W = 4, SiLU: 23 us (15.4 for the bytes),
+// the exponential and the reciprocal on the SFU 59 % busy and issue 65 %.  With
+// starts (2 x 1024 x 20011, W = 5, every 500): 63 us (25.0), the tests of the
+// taps and the unpacking of bf16 on the integer pipe.
 //
 // Backward: with q_t = dy_t (silu'(p_t)),
 //   dx_s = sum_j w_j q_(s + (W-1) - j),   dw_j = sum_t q_t x_(t - (W-1) + j),   dbias = sum_t q_t.
-// p is recomputed from x, for the W - 1 steps behind a thread's own as well.
+// p is recomputed from x; q of the W - 1 steps behind a thread's own comes
+// from the next thread through shared memory, and for the block's last thread
+// from the round before: a block works its spans from the last to the first
+// (each thread computing them itself: 51.9 us where this takes 47, 8 x 1536 x
+// 2048 bf16, W = 4, SiLU; 23.1 for the bytes; 16 warps an SM at 109 registers
+// issue 52 % of the time).
 // dw and dbias sum over batch and steps for each channel, so a block (or a
 // cluster of blocks, when the channels are few) takes one channel and all of
 // its batch entries; every thread keeps its W + 1 sums in registers over all

@@ -35,13 +35,15 @@ cudaError_t fwd(cudaStream_t s, ConvParams &p) {
 
 template <int W>
 cudaError_t bwd(cudaStream_t s, ConvParams &p) {
-    // Blocks per channel: enough for about eight blocks per SM, no more than
-    // the channel's vectors feed.
+    // Blocks per channel: enough for four blocks per SM, which is what runs at
+    // once, no more than the channel's spans feed.  (fp32 4 x 1024 x 4096: 63
+    // us, 68 with eight per SM wanted and 78 with sixteen; bf16 2 x 1024 x 20011
+    // with starts 149, 172 and 201; 4 x 64 x 65536: 38 with each.)
     const int64_t vecs = p.batch * spans_of(p.L);
     p.small = vecs <= INT_MAX;
     p.by_spans = divisor_of(spans_of(p.L));
     int nblk = 1;
-    while (nblk < 8 && p.dim * nblk < (int64_t)layer_sm_count() * 8 && vecs > (int64_t)nblk * kConvBwdThreads) nblk *= 2;
+    while (nblk < 8 && p.dim * nblk < (int64_t)layer_sm_count() * 4 && vecs > (int64_t)nblk * kConvBwdThreads) nblk *= 2;
     const int threads = vecs < kConvBwdThreads ? (int)(vecs + 31) / 32 * 32 : kConvBwdThreads;
     p.rounds = (vecs + threads - 1) / threads;
     p.each = (p.rounds + nblk - 1) / nblk;

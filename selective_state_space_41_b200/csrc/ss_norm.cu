@@ -6,24 +6,29 @@
 //   dx = r (v - sum_d v / D - xh sum_d v xh / D) with v = dy w   (RMS: without the middle term)
 //   dw = sum dy xh,  db = sum dy  over all steps of the batch
 //
-// All four kernels are bound by memory: x is read once (backward: x and dy)
-// and a result written once, against some ten operations an element.  What a
-// row needs twice therefore stays in registers between its sums and its
-// results.
+// The traffic sets the floor: x is read once (backward: x and dy) and a result
+// written once, against some ten operations an element.  What a step needs
+// twice therefore stays on the chip between its sums and its results.  Which
+// kernel runs is a matter of shape (norm_plan):
 //
-// seqlen = 1 (rows of dim contiguous elements): a warp or a block takes a
-// row, 8-element vectors dealt out over its threads.  In the backward the
-// blocks stay and walk over the rows, so a thread keeps its columns, and
-// their parts of dw and db are sums in its registers.
+// Rows (seqlen = 1: dim contiguous elements): 32 to 512 threads take a row,
+// 8-element vectors dealt out over them.  In the backward the blocks stay and
+// walk over the rows, so a thread keeps its columns, and their parts of dw and
+// db are sums in its registers.
 //
-// seqlen > 1: the channels of a step lie L elements apart.  A lane takes one
-// step, a warp 32 steps of kNch channels: every access is then 32
-// neighbouring elements whatever L is, and the sums over channels stay
-// within the lane but for one exchange between the warps, and between the
-// blocks of a cluster when one block's registers do not hold dim channels.
-// The backward needs sums over the steps as well; those of 32 channels come
-// out of 31 shuffles (each round halves the values a lane still holds and
-// doubles the lanes they sum over) and stay with lane i for channel i.
+// Tiles (seqlen > 1, rows of whole vectors, all channels of 64 bytes' worth of
+// steps fit into shared memory): a block copies its next tile in under the
+// results of the present one.
+//
+// Clusters (seqlen > 1 otherwise): the channels of a step lie L elements
+// apart.  A warp takes 32 channels of 32 steps (or of 64 or 32 in vectors)
+// into registers; the sums over channels need one exchange between the warps
+// and one between the blocks of a cluster, where one block's registers do not
+// hold dim channels.  The backward's sums over the steps come out of shuffles
+// that halve the values a lane still holds and double the lanes they sum over.
+//
+// Wide (dim beyond what a block or a cluster holds): passes over the row or
+// tile, the later ones from the caches.
 //
 // dw and db leave each block (or cluster) as one row of partial sums in the
 // workspace; a second kernel adds the rows in a fixed order, so the results
@@ -152,7 +157,9 @@ __device__ __forceinline__ float2 there(float2 v, int k, int i, int t, int T, in
 }
 
 // T threads a row, blockDim / T rows a block at a time; the next row is on
-// its way while one is worked on.
+// its way while one is worked on.  8 rows of 768 bf16: 4.1 us, a launch and a
+// chain of two sums; 16384 rows: 14.4 us (3.5 TB/s), the latency of a
+// row's loads and sums.
 template <typename Tin, typename Tout, int kNv, bool kVec>
 __global__ void __launch_bounds__(512) norm_rows_fwd_kernel(const NormParams p, int T) {
     __shared__ float red[2][2][16][1];
@@ -242,7 +249,9 @@ __global__ void __launch_bounds__(1024) norm_rows_fwd_wide_kernel(const NormPara
 
 // Blocks stay and walk over the rows.  A thread's columns are the same in
 // every row, so their parts of dw and db are sums in its registers, joined
-// over the block's groups at the end.
+// over the block's groups at the end.  16384 rows of 768 bf16: 25 us with
+// the second kernel's 5 or so, against 11.6 for the bytes: 16 warps an SM (128
+// registers) do not cover the loads, and their sums issue 47 % of the time.
 template <typename Tin, typename Tout, int kNv, bool kVec>
 __global__ void __launch_bounds__(512) norm_rows_bwd_kernel(const NormParams p, int T) {
     extern __shared__ float acc[];  // groups x 2 x dim
@@ -544,7 +553,9 @@ __device__ __forceinline__ float2 join(const float2 *part, int stride, int parts
 // stages, always as mean and squares about it (no difference of large sums):
 // a warp's channels, the block's warps, the cluster's blocks; each block
 // writes its own into every other's shared memory, so one cluster barrier is
-// all they wait for.
+// all they wait for.  Single steps (8 x 1536 x 2047 bf16): 64 us, bound by
+// the instructions of two-byte accesses and by the barriers (issue 53 %); in
+// vectors 35 us for 2048 steps, where the tiles below take 30.
 template <typename Tin, typename Tout, int V, int kMaxW>
 __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 3 : 1) norm_steps_fwd_kernel(const NormParams p, int nblk) {
     using G = Tile<V>;
@@ -670,7 +681,9 @@ __device__ __forceinline__ float lane_sums(float (&v)[kN], int lane) {
     return v[0];
 }
 
-// Backward over steps: clusters stay and walk over the tiles.
+// Backward over steps: clusters stay and walk over the tiles.  3 x 1000 x 4099
+// fp32: 55 us with the second kernel's 5 or so, against 22.5 for the bytes:
+// 16 warps an SM and a cluster barrier for each 32 steps (issue 45 %).
 template <typename Tin, typename Tout, int V, int kMaxW>
 __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 2 : 1) norm_steps_bwd_kernel(const NormParams p, int nblk) {
     using G = Tile<V>;
@@ -915,6 +928,9 @@ __device__ __forceinline__ void for_batches(int batches, int full, F f) {
 // The pivot is a mean of n0 of the thread's own n values, so its square
 // distance from their mean is at most S / n0: sum d^2 is at most
 // (1 + n / n0) S, and nothing is lost in the difference, whatever the values.
+//
+// 8 x 1536 x 2048 bf16: 30 us (15.4 for the bytes).  Two blocks an SM have
+// 512 tiles in 2 rounds where 1.73 would be even, and issue 52 % of the time.
 template <typename Tin, typename Tout>
 __global__ void __launch_bounds__(32 * kTileWarps, 2) norm_tile_fwd_kernel(const NormParams p, int batches) {
     using G = Geo<Tin>;
@@ -1039,7 +1055,8 @@ __global__ void __launch_bounds__(32 * kTileWarps, 2) norm_tile_fwd_kernel(const
 }
 
 // Backward: x and dy, and the block's sums of dw and db per channel, in
-// shared memory.
+// shared memory, which leaves one block an SM: 8 x 1536 x 2048 bf16 53 us
+// with the second kernel (23.1 for the bytes).
 template <typename T>
 __global__ void __launch_bounds__(32 * kTileWarps, 1) norm_tile_bwd_kernel(const NormParams p, int batches) {
     using G = Geo<T>;
@@ -1317,6 +1334,9 @@ NormPlan norm_plan(const ss_desc *desc, bool vec, bool back) {
         // The fewest threads that hold a row with three vectors each at most
         // (two where elements are loaded one by one and cost more registers):
         // the backward's sums, parameters and inputs then stay in 128 registers.
+        // (Backward of 16384 rows of 768 bf16: 25 us, 31 with two vectors at
+        // most, 43 with one; 16001 rows of 1001, element by element: 59, 67
+        // with one.)
         const int64_t vecs = (desc->dim + kV - 1) / kV, most = vec ? 3 : 2;
         pl.T = 32;
         while (pl.T < 512 && vecs > (int64_t)pl.T * most) pl.T *= 2;
@@ -1331,7 +1351,9 @@ NormPlan norm_plan(const ss_desc *desc, bool vec, bool back) {
     const int64_t n = desc->batch * desc->seqlen;
     // Tiles of 64 bytes of every channel in shared memory, while they fit:
     // the channels over T threads, in batches of T.  (8 x 1536 x 2048 bf16:
-    // forward 31 us against 37 in clusters, backward 51 against 69; with rows
+    // forward 30 us against 36 in clusters, backward 53 against 69, with 256
+    // threads 35 and 67; fp32 4 x 1024 x 4096 forward 33 against 41; 4 x 256 x
+    // 16384 backward 38 against 36; with rows
     // that are not whole vectors the same scheme with 4- or 2-byte units took
     // 69 against 67 and 148 against 137, fp32 of 1000 x 4099 backward 65
     // against 55: those go to the clusters.)  The backward has dy in x's type;
@@ -1348,7 +1370,9 @@ NormPlan norm_plan(const ss_desc *desc, bool vec, bool back) {
         pl.blocks = pl.parts = tiles < resident * sms ? tiles : resident * sms;
         return pl;
     }
-    // The channels in the registers of up to 8 blocks of 8 warps, or of 16.
+    // The channels in the registers of up to 8 blocks of 8 warps, or of 16
+    // where 8 do not hold them (8 x 1536 x 2047 bf16 with blocks of 16: forward
+    // 90 us against 64, backward 98 against 96).
     const int64_t need = (desc->dim + kWarpCh - 1) / kWarpCh;
     pl.max_warps = need <= 64 ? 8 : 16;
     const int64_t nblk = (need + pl.max_warps - 1) / pl.max_warps;
