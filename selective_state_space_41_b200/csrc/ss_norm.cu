@@ -1276,8 +1276,14 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const float *part, int6
     const int64_t c = (int64_t)blockIdx.x * 32 + tx;
     float s = 0.f;
     if (c < 2 * dim) {
-#pragma unroll 8
-        for (int64_t k = ty; k < parts; k += 32) s += part[k * 2 * dim + c];
+        constexpr int kAt = 10;  // loads in flight
+        for (int64_t k = ty; k < parts; k += 32 * kAt) {
+            float v[kAt];
+#pragma unroll
+            for (int i = 0; i < kAt; ++i) v[i] = part[min(k + 32 * i, parts - 1) * 2 * dim + c];
+#pragma unroll
+            for (int i = 0; i < kAt; ++i) s += k + 32 * i < parts ? v[i] : 0.f;
+        }
     }
     sm[ty][tx] = s;
     __syncthreads();
