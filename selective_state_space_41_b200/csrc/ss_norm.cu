@@ -20,8 +20,8 @@
 // steps fit into shared memory): a block copies its next tile in under the
 // results of the present one.
 //
-// Clusters (seqlen > 1 otherwise): the channels of a step lie L elements
-// apart.  A warp takes 32 channels of 32 steps (or of 64 or 32 in vectors)
+// Clusters (seqlen > 1 otherwise; in words of two steps where that pays): the
+// channels of a step lie L elements apart.  A warp takes 32 channels of 32 steps (or of 64 or 32 in vectors)
 // into registers; the sums over channels need one exchange between the warps
 // and one between the blocks of a cluster, where one block's registers do not
 // hold dim channels.  The backward's sums over the steps come out of shuffles
@@ -553,9 +553,10 @@ __device__ __forceinline__ float2 join(const float2 *part, int stride, int parts
 // stages, always as mean and squares about it (no difference of large sums):
 // a warp's channels, the block's warps, the cluster's blocks; each block
 // writes its own into every other's shared memory, so one cluster barrier is
-// all they wait for.  Single steps (8 x 1536 x 2047 bf16): 64 us, bound by
-// the instructions of two-byte accesses and by the barriers (issue 53 %); in
-// vectors 35 us for 2048 steps, where the tiles below take 30.
+// all they wait for.  Single steps (fp32 3 x 1000 x 4099): 35 us,
+// 15 for the bytes, the instructions of four-byte accesses and the barriers
+// (issue 53 %); in vectors 36 us for 8 x 1536 x 2048 bf16, where the tiles
+// below take 30.
 template <typename Tin, typename Tout, int V, int kMaxW>
 __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 3 : 1) norm_steps_fwd_kernel(const NormParams p, int nblk) {
     using G = Tile<V>;
@@ -807,6 +808,166 @@ __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 2 : 1) norm_steps_bwd
         float *out = p.part + group * 2 * p.dim;
         out[c0 + sl * G::kLc] = dw;
         out[p.dim + c0 + sl * G::kLc] = db;
+    }
+}
+
+// ---------------------------------------------------------- steps in pairs
+//
+// The forward of bf16 rows that are not whole vectors, in words of two steps: a
+// lane takes a word of each of its warp's channels.  With an odd L the rows of
+// every other channel start in the middle of a word, so their words lie one
+// step earlier: those of channels c0, c0 + 2, ... cover steps 2i - sh[0] and
+// the next one, those of the others 2i - sh[1] (each 0 or 1).  Sums over
+// channels are kept for the two kinds apart and brought to steps 2i, 2i + 1 by
+// one shuffle at the end.  32 words so cover 63 steps of both kinds; tiles do
+// not cross batch entries, where a word's two steps are not neighbours.
+// (8 x 1536 x 2047: 53 us, 64 in single steps; fp32 3 x 1000 x 4099 took 41
+// against 35, and the backward, whose words fill the registers, 98 against 96:
+// those stay with single steps.)
+constexpr int kPairSteps = 63, kPairWarps = 8;
+using Half = __nv_bfloat16;
+
+// Where a warp's words lie.
+struct PairTile {
+    int64_t e0, index;  // element of channel c0 at the tile's first step; that step among all
+    int n, sh[2];       // steps of the tile, shifts of the two kinds of channels
+    bool last;          // the tensor's last step is in the tile
+    // Whether the steps of this lane's words of kind k are the tile's.
+    __device__ __forceinline__ bool x(int k, int lane) const { return 2 * lane >= sh[k] && 2 * lane - sh[k] < n; }
+    __device__ __forceinline__ bool y(int k, int lane) const { return 2 * lane - sh[k] + 1 < n; }
+    __device__ __forceinline__ int step(int k, int lane, int i) const { return min(max(2 * lane - sh[k] + i, 0), n - 1); }
+    // The lane's word of channel c0 + i, or the row's last one for a lane behind it.
+    __device__ __forceinline__ int64_t word(int i, int lane, int64_t L) const {
+        const int s = sh[i & 1];
+        return e0 + i * L - s + 2 * min(lane, (n - 1 + s) >> 1);
+    }
+};
+__device__ __forceinline__ PairTile pair_tile(const NormParams &p, uint32_t tile, int64_t c0) {
+    const uint32_t per = (uint32_t)((p.L + kPairSteps - 1) / kPairSteps), b = tile / per;
+    const int64_t s0 = (int64_t)(tile - b * per) * kPairSteps;
+    PairTile t;
+    t.e0 = ((int64_t)b * p.dim + c0) * p.L + s0;
+    t.index = b * p.L + s0;
+    t.n = (int)min((int64_t)kPairSteps, p.L - s0);
+    t.sh[0] = (int)(t.e0 & 1), t.sh[1] = (int)((t.e0 + p.L) & 1);
+    t.last = t.index + t.n == p.batch * p.L;
+    return t;
+}
+
+// The words of a warp's channels; zero where there is none.
+__device__ __forceinline__ void load_words(uint32_t (&r)[kWarpCh], const Half *p, const PairTile &t, int lane, int have,
+                                           const NormParams &q) {
+    if (have == kWarpCh && !t.last) {
+        const Half *a = p + t.word(0, lane, q.L), *b = p + t.word(1, lane, q.L);
+#pragma unroll
+        for (int i = 0; i < kWarpCh; ++i) r[i] = __ldg(reinterpret_cast<const uint32_t *>((i % 2 ? b : a) + (i / 2) * 2 * q.L));
+        return;
+    }
+    const int64_t n = q.batch * q.dim * q.L;
+#pragma unroll
+    for (int i = 0; i < kWarpCh; ++i) {
+        r[i] = 0u;
+        if (i < have) {
+            const int64_t e = t.word(i, lane, q.L);
+            if (e + 1 < n) r[i] = __ldg(reinterpret_cast<const uint32_t *>(p + e));
+            else r[i] = Io<Half>::bits(p, e);  // the tensor's last element has no next one
+        }
+    }
+}
+
+// Values of the words' steps 2 lane - sh, and one on, to those of steps
+// 2 lane, 2 lane + 1, and back (the last and the first are not the tile's).
+__device__ __forceinline__ float2 to_steps(float2 v, int sh) {
+    const float next = __shfl_down_sync(0xffffffffu, v.x, 1);
+    return sh ? make_float2(v.y, next) : v;
+}
+__device__ __forceinline__ float2 to_words(float2 v, int sh) {
+    const float before = __shfl_up_sync(0xffffffffu, v.y, 1);
+    return sh ? make_float2(before, v.x) : v;
+}
+
+__device__ __forceinline__ void put_word(float *p, float2 v, bool x, bool y) {
+    if (x && y) *reinterpret_cast<float2 *>(p) = v;
+    else if (x || y) put(p, y ? 1 : 0, y ? v.y : v.x);
+}
+__device__ __forceinline__ void put_word(Half *p, float2 v, bool x, bool y) {
+    if (x && y) *reinterpret_cast<uint32_t *>(p) = pack_bf16x2(v.x, v.y);
+    else if (x || y) put(p, y ? 1 : 0, y ? v.y : v.x);
+}
+
+// Forward, as norm_steps_fwd_kernel.  No step of a word is the other's
+// business, so nothing is masked before the results.
+template <typename Tout>
+__global__ void __launch_bounds__(32 * kPairWarps, 3) norm_pairs_fwd_kernel(const NormParams p, int nblk) {
+    constexpr int kN = kWarpCh;
+    __shared__ float2 part[kPairWarps][64], slot[8][64];
+    __shared__ float stat[2][64];  // -mean, 1 / deviation
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, rank = (int)(blockIdx.x % nblk);
+    if (nblk > 1) cluster_arrive();  // waited for before the first remote store
+    const int64_t wide = (int64_t)warps * kN, c0 = rank * wide + warp * kN;
+    const int have = (int)clamp_count(p.dim - c0, kN);
+    const PairTile at = pair_tile(p, blockIdx.x / nblk, c0);
+    uint32_t x[kN];
+    load_words(x, static_cast<const Half *>(p.x), at, lane, have, p);
+    const float2 none[2] = {both(0.f), both(0.f)};
+    float2 nm[2] = {none[0], none[1]}, S[2] = {none[0], none[1]};
+    float2 mean = both(0.f);
+    if (!p.rms && have > 0) {
+        float2 A[2] = {none[0], none[1]};
+#pragma unroll
+        for (int i = 0; i < kN; ++i) A[i & 1] = add2(A[i & 1], pair_of<Half>(x, i));
+        mean = mul2(add2(to_steps(A[0], at.sh[0]), to_steps(A[1], at.sh[1])), both(1.f / (float)have));
+        nm[0] = mul2(to_words(mean, at.sh[0]), both(-1.f)), nm[1] = mul2(to_words(mean, at.sh[1]), both(-1.f));
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        float2 d = add2(pair_of<Half>(x, i), nm[i & 1]);
+        if (i >= have) d = both(0.f);
+        S[i & 1] = fma2(d, d, S[i & 1]);
+    }
+    S[0] = add2(to_steps(S[0], at.sh[0]), to_steps(S[1], at.sh[1]));
+    part[warp][2 * lane] = make_float2(mean.x, S[0].x);
+    part[warp][2 * lane + 1] = make_float2(mean.y, S[0].y);
+    __syncthreads();
+    const int t = threadIdx.x;
+    float2 all = both(0.f);
+    if (t < 64) all = join(&part[0][t], 64, warps, [&](int k) { return clamp_count(p.dim - (rank * wide + k * kN), kN); });
+    if (nblk > 1) {
+        cluster_wait();  // every block has begun
+        if (t < 64)
+            for (int k = 0; k < nblk; ++k) peer_store(&slot[rank][t], k, all);
+        cluster_arrive();
+        cluster_wait();
+        if (t < 64) all = join(&slot[0][t], 64, nblk, [&](int k) { return clamp_count(p.dim - k * wide, wide); });
+    }
+    if (t < 64) {
+        const float rstd = rsqrtf(fmaf(all.y, p.inv_dim, p.eps));
+        stat[0][t] = -all.x, stat[1][t] = rstd;
+        if (rank == 0 && t < at.n) {
+            if (p.mean && !p.rms) p.mean[at.index + t] = all.x;
+            if (p.rstd) p.rstd[at.index + t] = rstd;
+        }
+    }
+    __syncthreads();
+    bool in_x[2], in_y[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int a = at.step(k, lane, 0), b = at.step(k, lane, 1);
+        nm[k] = make_float2(stat[0][a], stat[0][b]), S[k] = make_float2(stat[1][a], stat[1][b]);
+        in_x[k] = at.x(k, lane), in_y[k] = at.y(k, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) asm volatile("" : "+r"(x[i]));
+    Tout *y = static_cast<Tout *>(p.y);
+    Tout *to[2] = {y + at.word(0, lane, p.L), y + at.word(1, lane, p.L)};
+    int64_t apart = 2 * p.L;
+    again(apart);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        if (i < have) {
+            const float2 w = both(p.weight ? __ldg(p.weight + c0 + i) : 1.f), b = both(p.bias ? __ldg(p.bias + c0 + i) : 0.f);
+            put_word(to[i & 1] + (i / 2) * apart, fma2(mul2(add2(pair_of<Half>(x, i), nm[i & 1]), S[i & 1]), w, b), in_x[i & 1], in_y[i & 1]);
+        }
     }
 }
 
@@ -1302,7 +1463,7 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const float *part, int6
 // ------------------------------------------------------------------- host
 
 // The launch of a shape: kernel family, threads and blocks.
-enum NormKind { kRows, kRowsWide, kTile, kCluster, kStepsWide };
+enum NormKind { kRows, kRowsWide, kTile, kPairs, kCluster, kStepsWide };
 struct NormPlan {
     NormKind kind;
     bool vec;
@@ -1331,8 +1492,10 @@ int64_t tile_smem(int64_t dim, const NormPlan &pl, bool back) {
     return back ? 2 * units + 8 * dim : units;
 }
 
-// vec: the innermost axis is whole vectors at every base.
-NormPlan norm_plan(const ss_desc *desc, bool vec, bool back) {
+// What the innermost axis allows at every base: whole vectors, words of two steps.
+enum NormWords { kSingle, kWords, kVectors };
+NormPlan norm_plan(const ss_desc *desc, NormWords words, bool back) {
+    const bool vec = words == kVectors;
     NormPlan pl{};
     const int64_t sms = layer_sm_count();
     pl.vec = vec;
@@ -1376,10 +1539,23 @@ NormPlan norm_plan(const ss_desc *desc, bool vec, bool back) {
         pl.blocks = pl.parts = tiles < resident * sms ? tiles : resident * sms;
         return pl;
     }
+    // Words of two steps, the channels in the registers of up to 8 blocks of 8
+    // warps, unless tiles that end with the row leave over a fifth of the lanes
+    // without a step, or there are too few of them to go round (1 x 500 x 1001:
+    // 10.4 us against 8.3 in single steps, whose tiles are half as long).
+    const int64_t need = (desc->dim + kWarpCh - 1) / kWarpCh;
+    const int64_t row_tiles = (desc->seqlen + kPairSteps - 1) / kPairSteps;
+    pl.blocks = desc->batch * row_tiles, pl.nblk = (int)((need + kPairWarps - 1) / kPairWarps);
+    if (words == kWords && !back && desc->in_dtype == SS_BF16 && pl.nblk <= 8 &&
+        row_tiles * kPairSteps * 4 <= desc->seqlen * 5 && pl.blocks * pl.nblk >= 2 * sms) {
+        pl.kind = kPairs;
+        pl.warps = (int)((need + pl.nblk - 1) / pl.nblk);
+        if (pl.warps < 2) pl.warps = 2;  // a thread for each step of the tile
+        return pl;
+    }
     // The channels in the registers of up to 8 blocks of 8 warps, or of 16
     // where 8 do not hold them (8 x 1536 x 2047 bf16 with blocks of 16: forward
     // 90 us against 64, backward 98 against 96).
-    const int64_t need = (desc->dim + kWarpCh - 1) / kWarpCh;
     pl.max_warps = need <= 64 ? 8 : 16;
     const int64_t nblk = (need + pl.max_warps - 1) / pl.max_warps;
     if (nblk <= 8) {
@@ -1405,12 +1581,15 @@ NormPlan norm_plan(const ss_desc *desc, bool vec, bool back) {
     return pl;
 }
 
-// Whole vectors: rows of dim elements, or steps of each channel.  (The tile
-// kernels read their parameters one by one, the row kernels in vectors.)
-bool norm_vec(const ss_desc *desc, std::initializer_list<const void *> tensors, std::initializer_list<const void *> params) {
+// Whole vectors: rows of dim elements, or steps of each channel.  (The kernels
+// over the steps read their parameters one by one, the row kernels in vectors.)
+NormWords norm_words(const ss_desc *desc, std::initializer_list<const void *> tensors, std::initializer_list<const void *> params) {
     const int64_t inner = desc->seqlen == 1 ? desc->dim : desc->seqlen;
     const int64_t whole = desc->seqlen == 1 || desc->in_dtype == SS_BF16 ? 8 : 4;
-    return inner % whole == 0 && vec_ok(tensors) && (desc->seqlen > 1 || vec_ok(params));
+    if (inner % whole == 0 && vec_ok(tensors) && (desc->seqlen > 1 || vec_ok(params))) return kVectors;
+    for (const void *q : tensors)
+        if (!layer_aligned(q, 2 * layer_size(desc->out_dtype))) return kSingle;
+    return kWords;
 }
 
 template <typename K>
@@ -1487,6 +1666,10 @@ cudaError_t dispatch_norm(bool back, const NormPlan &pl, cudaStream_t s, const N
                    : pl.nv == 2 ? launch_rows<Tin, Tout, 2, true>(back, pl, s, p)
                                 : launch_rows<Tin, Tout, 3, true>(back, pl, s, p);
         case kTile: return launch_tile<Tin, Tout>(back, pl, s, p);
+        case kPairs:
+            if constexpr (sizeof(Tin) == 2)
+                return launch_cluster(norm_pairs_fwd_kernel<Tout>, pl.blocks * pl.nblk, 32 * pl.warps, pl.nblk, s, p);
+            break;
         default: break;
     }
     if (pl.max_warps == 8)
@@ -1531,16 +1714,20 @@ ss_status ss_norm_fwd(const ss_desc *desc, const void *x, const float *weight, c
     NormParams p = norm_params(desc);
     p.x = x, p.weight = weight, p.bias = bias, p.y = y, p.mean = mean, p.rstd = rstd;
     p.eps = eps, p.rms = rms != 0;
-    const NormPlan pl = norm_plan(desc, norm_vec(desc, {x, y}, {weight, bias}), false);
+    const NormPlan pl = norm_plan(desc, norm_words(desc, {x, y}, {weight, bias}), false);
     return status_of(SS_LAYER_DISPATCH(desc, dispatch_norm)(false, pl, reinterpret_cast<cudaStream_t>(stream), p));
 }
 
 size_t ss_norm_bwd_workspace_bytes(const ss_desc *desc) {
     LayerSizes sz;
     if (check_norm(desc, &sz) != SS_OK || sz.elems == 0) return 0;
-    // the larger of the two shapes: which one runs depends on the pointers too
-    const int64_t a = norm_plan(desc, false, true).parts, b = norm_plan(desc, true, true).parts;
-    return (size_t)(a > b ? a : b) * 2 * (size_t)desc->dim * sizeof(float);
+    // the largest of the shapes: which one runs depends on the pointers too
+    int64_t most = 0;
+    for (const NormWords w : {kSingle, kVectors}) {  // (words of two steps: the forward alone)
+        const int64_t parts = norm_plan(desc, w, true).parts;
+        most = parts > most ? parts : most;
+    }
+    return (size_t)most * 2 * (size_t)desc->dim * sizeof(float);
 }
 
 ss_status ss_norm_bwd(const ss_desc *desc, const void *x, const float *weight, const float *mean, const float *rstd,
@@ -1570,7 +1757,7 @@ ss_status ss_norm_bwd(const ss_desc *desc, const void *x, const float *weight, c
     }
     p.x = x, p.weight = weight, p.mean_in = mean, p.rstd_in = rstd, p.dy = dy, p.dx = dx;
     p.part = static_cast<float *>(workspace);
-    const NormPlan pl = norm_plan(desc, norm_vec(desc, {x, dy, dx}, {weight}), true);  // the workspace is aligned
+    const NormPlan pl = norm_plan(desc, norm_words(desc, {x, dy, dx}, {weight}), true);  // the workspace is aligned
     cudaError_t e = SS_LAYER_DISPATCH(desc, dispatch_norm)(true, pl, s, p);
     if (e == cudaSuccess && p.sums) {
         norm_sums_kernel<<<(unsigned)((2 * p.dim + 31) / 32), 1024, 0, s>>>(p.part, pl.parts, p.dim, dweight, dbias);

@@ -238,3 +238,34 @@ def test_workspace_elsewhere_is_refused():
     with pytest.raises(ss.SelscanError):
         ss.ss_norm_bwd(x, x, rstd, dx, dweight=dw, workspace=torch.empty(n - 4, dtype=torch.uint8, device="cuda"))
     ss.ss_norm_bwd(x, x, rstd, dx, dweight=dw, workspace=torch.empty(n, dtype=torch.uint8, device="cuda"))
+
+
+# Rows that are not whole vectors, in words of two steps: rows that start in
+# the middle of a word or not, tiles of 63 steps and their ends, a tensor that
+# ends with half a word, channels that fill no warp or several blocks.
+@pytest.mark.parametrize("B,D,L", [(300, 1, 63), (301, 3, 61), (150, 31, 126), (101, 33, 127), (150, 17, 125), (100, 64, 189),
+                                   (61, 255, 315), (25, 257, 317), (25, 1000, 133), (1, 1001, 4723), (41, 2047, 61), (100, 768, 62),
+                                   (10, 1024, 442), (1, 2, 18901)])
+@pytest.mark.parametrize("types", TYPES)
+def test_words_of_two_steps(B, D, L, types):
+    run(B, D, L, *types, rms=D % 3 == 0, seed=D + L)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_nonfinite_in_words(dtype):
+    """A NaN in one half of a word stays out of the other step, of the next
+    tile and of the gradients of other batch entries."""
+    B, D, L = 101, 40, 127
+    x = rand(B, D, L, seed=41, dtype=dtype)
+    y0, m0, r0 = ss.layer_norm_fwd(x.cuda(), return_stats=True)
+    bad = torch.zeros(B, L, dtype=torch.bool)
+    for b, d, t in ((0, 3, 0), (0, 4, 62), (0, 5, 63), (1, 6, 126), (1, 7, 40)):
+        x[b, d, t], bad[b, t] = float("nan"), True
+    y, m, r = ss.layer_norm_fwd(x.cuda(), return_stats=True)
+    bad3 = bad[:, None].expand(B, D, L)
+    assert y.cpu()[bad3].isnan().all() and torch.equal(y.cpu()[~bad3], y0.cpu()[~bad3])
+    assert torch.equal(r.isnan().cpu(), bad)
+    dy = rand(B, D, L, seed=42, dtype=dtype)
+    g0 = ss.layer_norm_bwd(rand(B, D, L, seed=41, dtype=dtype).cuda(), dy.cuda(), r0, mean=m0)
+    g = ss.layer_norm_bwd(x.cuda(), dy.cuda(), r, mean=m)
+    assert torch.equal(g["dx"].cpu()[~bad3], g0["dx"].cpu()[~bad3]) and g["dx"].cpu()[bad3].isnan().all()
