@@ -9,7 +9,7 @@
 // and some twenty operations: the kernels are bound by memory, and close
 // behind it by the instructions they issue.  What the design has to do is to
 // keep enough loads in flight, the serial chain of the recurrence short and
-// the work per step small (4 x 1024 x 100000 bf16: 463 us, 375 for the
+// the work per step small (4 x 1024 x 100000 bf16: 459 us, 375 for the
 // bytes; 8 x 1536 x 2048 with the output gate, forward 42 and backward 73,
 // 30.7 and 53.7 for the bytes; issue 55 to 60 %).  G lanes take a row (32, or fewer for short rows),
 // 16 steps each at a time forward and 8 backward.  Each lane folds its steps
@@ -19,7 +19,8 @@
 // the G lanes' steps it gives the state entering the lane's own, from which
 // the lane runs its steps again, now one after the other as the formula has
 // them.  W warps share a row when there are few rows: each folds its own
-// steps, and W pairs in shared memory join them.  The loads of the next steps
+// steps, and W pairs in shared memory join them (of a cluster's blocks, where
+// rows are very few: each warp writes its pair to all of them).  The loads of the next steps
 // are issued before the current ones are worked on; gates and products are
 // computed in pairs of steps with the packed arithmetic of two floats.
 //
@@ -44,7 +45,8 @@ namespace selscan {
 namespace {
 
 constexpr int kPiece = 256;    // steps between two checkpoints of a row
-constexpr int kMaxWarps = 16;  // warps sharing a row
+constexpr int kMaxWarps = 16;  // warps of a block sharing a row
+constexpr int kMaxBlocks = 8;  // blocks sharing one: a cluster
 
 struct GlrParams {
     const void *x, *g, *z, *dy;
@@ -126,10 +128,32 @@ __device__ __forceinline__ void scan_down(float &A, float &B, int lane, int lane
     }
 }
 
+enum Share { kOwn, kBlock, kCluster };  // who shares a row
+
 struct Pair {
     float A, B;
     int cut;
 };
+
+// A warp's pair (from its first lanes) to all blocks that share its row, and
+// the meeting of their warps.
+template <int kShare>
+__device__ __forceinline__ void share(Pair *to, const Pair &q, int lane, int nblk) {
+    if constexpr (kShare == kBlock) {
+        if (lane == 0) *to = q;
+        __syncthreads();
+        return;
+    }
+    if (lane < nblk) {
+        uint32_t at;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(to)), "r"(lane));
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(q.A) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 4), "f"(q.B) : "memory");
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at + 8), "r"(q.cut) : "memory");
+    }
+    cluster_arrive();
+    cluster_wait();
+}
 
 // Vectors of a lane in the forward: 16 steps of bf16 halve what the scan over
 // the lanes costs a step (8 x 1536 x 2048: 37.5 us against 39), and would
@@ -143,11 +167,11 @@ struct Row {
     int shift;
     bool there;
 };
-template <bool kShared>
-__device__ __forceinline__ Row row_of(const GlrParams &p, int lanes) {
+template <int kShare>
+__device__ __forceinline__ Row row_of(const GlrParams &p, int lanes, int nblk) {
     Row r;
-    const int per = kShared ? 1 : (int)blockDim.x / lanes;  // rows of a block
-    r.row = kShared ? blockIdx.x : (int64_t)blockIdx.x * per + (int)threadIdx.x / lanes;
+    const int per = kShare != kOwn ? 1 : (int)blockDim.x / lanes;  // rows of a block
+    r.row = kShare == kCluster ? blockIdx.x / nblk : kShare == kBlock ? blockIdx.x : (int64_t)blockIdx.x * per + (int)threadIdx.x / lanes;
     r.there = r.row < p.rows;
     if (!r.there) r.row = p.rows - 1;  // lanes that only take part in their warp's shuffles
     const int64_t e0 = r.row * p.L;
@@ -164,15 +188,20 @@ __device__ __forceinline__ void bounds_of(const Row &r, int64_t v, int &lo, int 
     hi = left >= kV ? kV : left > 0 ? (int)left : 0;
 }
 
-// kShared: the block's warps share a row; otherwise every kG lanes (kG 0:
+// kShare: the warps of a block, or of a cluster of nblk, share a row; otherwise every kG lanes (kG 0:
 // `lanes`) have a row of their own.
-template <typename Tin, typename Tout, bool kZ, bool kR, bool kShared, int kG>
-__global__ void __launch_bounds__(512) glr_fwd_kernel(const GlrParams p, int lanes) {
+template <typename Tin, typename Tout, bool kZ, bool kR, int kShare, int kG>
+__global__ void __launch_bounds__(512) glr_fwd_kernel(const GlrParams p, int lanes, int nblk) {
     constexpr int kVecs = kGlrVecs<Tin>, kE = kVecs * kV;  // steps of a lane
-    __shared__ Pair pairs[2][kMaxWarps];
+    __shared__ Pair pairs[2][kShare == kCluster ? kMaxWarps * kMaxBlocks : kMaxWarps];
     const int G = kG ? kG : lanes, lane = threadIdx.x & 31, in = lane & (G - 1);
-    const int W = kShared ? (int)blockDim.x >> 5 : 1, w = kShared ? (int)threadIdx.x >> 5 : 0;
-    const Row r = row_of<kShared>(p, G);
+    const int wb = (int)blockDim.x >> 5, W = kShare == kOwn ? 1 : kShare == kBlock ? wb : wb * nblk;
+    const int w = (kShare == kOwn ? 0 : (int)threadIdx.x >> 5) + (kShare == kCluster ? (int)(blockIdx.x % nblk) * wb : 0);
+    const Row r = row_of<kShare>(p, G, nblk);
+    if constexpr (kShare == kCluster) {  // every block has begun before the first remote store
+        cluster_arrive();
+        cluster_wait();
+    }
     const int64_t bl = kR ? r.row / p.dim * p.L - r.shift : 0, bl_all = kR ? p.rows / p.dim * p.L : 0;
     const Tin *x = static_cast<const Tin *>(p.x) + r.base, *g = static_cast<const Tin *>(p.g) + r.base;
     const Tin *z = kZ ? static_cast<const Tin *>(p.z) + r.base : nullptr;
@@ -258,9 +287,8 @@ __global__ void __launch_bounds__(512) glr_fwd_kernel(const GlrParams p, int lan
         if (in == 0) Ax = 1.f, Bx = 0.f;
 
         float from = carry;  // the state entering this warp's steps
-        if constexpr (kShared) {
-            if (lane == 0) pairs[buf][w] = {Aw, Bw, any ? 1 : 0};
-            __syncthreads();
+        if constexpr (kShare != kOwn) {
+            share<kShare>(&pairs[buf][w], {Aw, Bw, any ? 1 : 0}, lane, nblk);
             float c = carry;
             for (int k = 0; k < W; ++k) {
                 if (k == w) from = c;
@@ -300,12 +328,17 @@ __global__ void __launch_bounds__(512) glr_fwd_kernel(const GlrParams p, int lan
     if (p.last && r.there && in == 0 && w == 0) p.last[r.row] = carry;
 }
 
-template <typename Tin, typename Tout, bool kZ, bool kR, bool kShared, int kG>
-__global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p, int lanes) {
-    __shared__ Pair pairs[2][kMaxWarps];
+template <typename Tin, typename Tout, bool kZ, bool kR, int kShare, int kG>
+__global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p, int lanes, int nblk) {
+    __shared__ Pair pairs[2][kShare == kCluster ? kMaxWarps * kMaxBlocks : kMaxWarps];
     const int G = kG ? kG : lanes, lane = threadIdx.x & 31, in = lane & (G - 1);
-    const int W = kShared ? (int)blockDim.x >> 5 : 1, w = kShared ? (int)threadIdx.x >> 5 : 0;
-    const Row r = row_of<kShared>(p, G);
+    const int wb = (int)blockDim.x >> 5, W = kShare == kOwn ? 1 : kShare == kBlock ? wb : wb * nblk;
+    const int w = (kShare == kOwn ? 0 : (int)threadIdx.x >> 5) + (kShare == kCluster ? (int)(blockIdx.x % nblk) * wb : 0);
+    const Row r = row_of<kShare>(p, G, nblk);
+    if constexpr (kShare == kCluster) {  // every block has begun before the first remote store
+        cluster_arrive();
+        cluster_wait();
+    }
     const int64_t bl = kR ? r.row / p.dim * p.L - r.shift : 0, bl_all = kR ? p.rows / p.dim * p.L : 0;
     const Tin *x = static_cast<const Tin *>(p.x) + r.base, *g = static_cast<const Tin *>(p.g) + r.base;
     const Tin *z = kZ ? static_cast<const Tin *>(p.z) + r.base : nullptr;
@@ -413,9 +446,8 @@ __global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p, int lan
         if (lane == last) Amx = 1.f, Mx = 0.f;
 
         float from = carry;  // the adjoint reaching this warp's steps from behind
-        if constexpr (kShared) {
-            if (lane == 0) pairs[buf][w] = {Aw, Mw, any ? 1 : 0};
-            __syncthreads();
+        if constexpr (kShare != kOwn) {
+            share<kShare>(&pairs[buf][w], {Aw, Mw, any ? 1 : 0}, lane, nblk);
             float c = carry;
             for (int k = W - 1; k >= 0; --k) {
                 if (k == w) from = c;
@@ -505,18 +537,30 @@ int64_t pieces(int64_t L) { return (L + kV - 1 + kPiece - 1) / kPiece; }
 // 1024 x 100000 bf16: 463, 521, 458), no more than the row feeds with
 // `per_lane` steps a lane.
 struct GlrShape {
-    int lanes, warps;
+    int lanes, warps, nblk;
 };
 GlrShape glr_shape(int64_t rows, int64_t L, int per_lane) {
     constexpr int kWant = 32;
     const int64_t steps = L + kV - 1, want = (int64_t)layer_sm_count() * kWant;
-    GlrShape s{32, 1};
+    GlrShape s{32, 1, 1};
     if (steps <= 16 * per_lane) {  // a row's steps in one turn
         s.lanes = 4;
         while (s.lanes * per_lane < steps) s.lanes *= 2;
         return s;
     }
     while (s.warps < kMaxWarps && rows * s.warps < want && (int64_t)s.warps * 32 * per_lane < steps) s.warps *= 2;
+    // Rows too few for the SMs are cut further, over a cluster of blocks, while
+    // all clusters run at once (one lies within one of the eight groups of SMs,
+    // which are not all of a size) and each block keeps three rounds of steps.
+    // (1 x 16 x 100000 bf16 with the gate, forward: 16.5 us, 31 with a block to
+    // a row; 1 x 64 x 300000: 57, 74; 1 x 4 x 200000, forward and backward: 52,
+    // 125; with fewer rounds, 1 x 37 x 20000: 27, 19.)
+    const int64_t sms = layer_sm_count();
+    while (s.warps == kMaxWarps && s.nblk < kMaxBlocks) {
+        const int64_t n = s.nblk * 2, resident = n == 2 ? sms / 2 : sms / 8 / n * 8 * 92 / 100;
+        if (rows > resident || n * kMaxWarps * 32 * per_lane * 3 > steps) break;
+        s.nblk = (int)n;
+    }
     return s;
 }
 
@@ -525,17 +569,30 @@ cudaError_t launch_glr(bool back, cudaStream_t s, const GlrParams &p) {
     const GlrShape q = glr_shape(p.rows, p.L, back ? kV : kGlrVecs<Tin> * kV);
     constexpr int kThreads = 128;
     const int64_t per = kThreads / q.lanes;
-    const unsigned grid = (unsigned)(q.warps > 1 ? p.rows : (p.rows + per - 1) / per);
+    const unsigned grid = (unsigned)(q.warps > 1 ? p.rows * q.nblk : (p.rows + per - 1) / per);
     const int threads = q.warps > 1 ? 32 * q.warps : kThreads;
     if (q.lanes < 32) {
-        if (back) glr_bwd_kernel<Tin, Tout, kZ, kR, false, 0><<<grid, threads, 0, s>>>(p, q.lanes);
-        else glr_fwd_kernel<Tin, Tout, kZ, kR, false, 0><<<grid, threads, 0, s>>>(p, q.lanes);
+        if (back) glr_bwd_kernel<Tin, Tout, kZ, kR, kOwn, 0><<<grid, threads, 0, s>>>(p, q.lanes, 1);
+        else glr_fwd_kernel<Tin, Tout, kZ, kR, kOwn, 0><<<grid, threads, 0, s>>>(p, q.lanes, 1);
     } else if (q.warps == 1) {
-        if (back) glr_bwd_kernel<Tin, Tout, kZ, kR, false, 32><<<grid, threads, 0, s>>>(p, 32);
-        else glr_fwd_kernel<Tin, Tout, kZ, kR, false, 32><<<grid, threads, 0, s>>>(p, 32);
+        if (back) glr_bwd_kernel<Tin, Tout, kZ, kR, kOwn, 32><<<grid, threads, 0, s>>>(p, 32, 1);
+        else glr_fwd_kernel<Tin, Tout, kZ, kR, kOwn, 32><<<grid, threads, 0, s>>>(p, 32, 1);
+    } else if (q.nblk > 1) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3((unsigned)threads);
+        cfg.stream = s;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = (unsigned)q.nblk;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        return back ? cudaLaunchKernelEx(&cfg, glr_bwd_kernel<Tin, Tout, kZ, kR, kCluster, 32>, p, 32, q.nblk)
+                    : cudaLaunchKernelEx(&cfg, glr_fwd_kernel<Tin, Tout, kZ, kR, kCluster, 32>, p, 32, q.nblk);
     } else {
-        if (back) glr_bwd_kernel<Tin, Tout, kZ, kR, true, 32><<<grid, threads, 0, s>>>(p, 32);
-        else glr_fwd_kernel<Tin, Tout, kZ, kR, true, 32><<<grid, threads, 0, s>>>(p, 32);
+        if (back) glr_bwd_kernel<Tin, Tout, kZ, kR, kBlock, 32><<<grid, threads, 0, s>>>(p, 32, 1);
+        else glr_fwd_kernel<Tin, Tout, kZ, kR, kBlock, 32><<<grid, threads, 0, s>>>(p, 32, 1);
     }
     return cudaGetLastError();
 }

@@ -136,6 +136,9 @@ __device__ __forceinline__ void store8(T *p, int64_t e, int lo, int hi, bool vec
     }
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 __device__ __forceinline__ int clamp8(int64_t v) { return v < 0 ? 0 : v > kV ? kV : (int)v; }
 
 // 1 / (1 + exp(-v)) of two values: exponential (2 ulp) and reciprocal (1 ulp)

@@ -382,9 +382,6 @@ __global__ void __launch_bounds__(1024) norm_rows_bwd_wide_kernel(const NormPara
 
 constexpr int kWarpCh = 32;  // channels of a warp
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
 // v into the same place of block `rank`'s shared memory.
 __device__ __forceinline__ void peer_store(float2 *p, int rank, float2 v) {
     uint32_t peer;

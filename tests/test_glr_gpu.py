@@ -208,3 +208,22 @@ def test_autograd(flags):
         y2 = ss.gated_recurrence_fn(x, g, z, *flags, initial_state=h0, reset=reset)
     assert torch.equal(y2, y) and not y2.requires_grad
     ss.gated_recurrence_fn(x, g, None, *flags).sum().backward()  # a broadcast gradient
+
+
+@pytest.mark.parametrize("B,D,L,every,dtype", [(1, 1, 50003, 0, BF), (1, 1, 25001, 3000, F32), (1, 3, 24600, 900, BF),
+                                               (2, 5, 12301, 0, F32), (1, 40, 12300, 0, F32), (1, 74, 12289, 2000, F32)])
+def test_rows_over_several_blocks(B, D, L, every, dtype):
+    """Few long rows: the blocks of a cluster share one."""
+    run(B, D, L, dtype, every=every, seed=D, gated=D != 40)
+
+
+def test_same_bits_over_several_blocks():
+    """The same rows among few (clusters) and among many (a block each)."""
+    x, g = rand(1, 160, 100003, seed=3, dtype=BF).cuda(), rand(1, 160, 100003, seed=4, dtype=BF).cuda()
+    few = [t[:, :16].contiguous() for t in (x, g)]
+    y, last, ck = ss.gated_recurrence_fwd(x, g, return_last_state=True, return_ckpt=True)
+    yf, lf, ckf = ss.gated_recurrence_fwd(*few, return_last_state=True, return_ckpt=True)
+    assert torch.equal(y[:, :16], yf) and torch.equal(last[:, :16], lf)
+    d = ss.gated_recurrence_bwd(x, g, x, ck)
+    df = ss.gated_recurrence_bwd(*few, few[0], ckf)
+    assert torch.equal(d["dx"][:, :16], df["dx"]) and torch.equal(d["dg"][:, :16], df["dg"])
