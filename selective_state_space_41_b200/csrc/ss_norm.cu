@@ -416,8 +416,13 @@ struct Patch {
     __device__ __forceinline__ void load(const T *p, int64_t apart, int have) {
         if constexpr (V == 1) {
             uint32_t b[G::kN];
+            if (have == G::kN) {
 #pragma unroll
-            for (int i = 0; i < G::kN; ++i) b[i] = Io<T>::bits(p + min(i, max(have - 1, 0)) * apart, 0);
+                for (int i = 0; i < G::kN; ++i, p += apart) b[i] = Io<T>::bits(p, 0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < G::kN; ++i) b[i] = Io<T>::bits(p + min(i, max(have - 1, 0)) * apart, 0);
+            }
 #pragma unroll
             for (int i = 0; i < G::kN; ++i) {
                 if constexpr (sizeof(T) == 4) w[i] = b[i];
@@ -681,7 +686,8 @@ __device__ __forceinline__ float lane_sums(float (&v)[kN], int lane) {
 
 // Backward over steps: clusters stay and walk over the tiles.  3 x 1000 x 4099
 // fp32: 55 us with the second kernel's 5 or so, against 22.5 for the bytes:
-// 16 warps an SM and a cluster barrier for each 32 steps (issue 45 %).
+// 16 warps an SM and a cluster barrier for each 32 steps (issue 45 %).  8 x
+// 1536 x 2047 bf16: 80 us (95 where full warps too ask which channels there are).
 template <typename Tin, typename Tout, int V, int kMaxW>
 __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 2 : 1) norm_steps_bwd_kernel(const NormParams p, int nblk) {
     using G = Tile<V>;
@@ -719,11 +725,13 @@ __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 2 : 1) norm_steps_bwd
         x.keep(have);
         g.keep(at.in ? have : 0);
         float term[G::kN];
+        // (all: every channel of the thread is there)
+        const auto to_sums = [&](auto all) {
 #pragma unroll
         for (int q = 0; q < G::kPairs; q += kRun) {
             const int i = G::chan(q);
-            const bool second = V == 1 && i + 1 < have;
-            const float2 w = param<V>(p.weight, i < have ? wc + i * G::kLc : min(c0, p.dim - 1), second, 1.f);
+            const bool second = V == 1 && (all.value || i + 1 < have);
+            const float2 w = param<V>(p.weight, all.value || i < have ? wc + i * G::kLc : min(c0, p.dim - 1), second, 1.f);
             float2 sum = both(0.f);
 #pragma unroll
             for (int k = 0; k < kRun; ++k) {
@@ -735,6 +743,9 @@ __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 2 : 1) norm_steps_bwd
             if constexpr (V == 1) term[i] = sum.x, term[i + 1] = sum.y;
             else term[i] = sum.x + sum.y;
         }
+        };
+        if (have == G::kN) to_sums(std::true_type{});
+        else to_sums(std::false_type{});
         if (p.sums) dw += lane_sums<G::kN>(term, lane);
         lanes_sum<V>(s1), lanes_sum<V>(s2);
         if (cl == 0) {
@@ -783,11 +794,13 @@ __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 2 : 1) norm_steps_bwd
             s2[k] = mul2(mul2(make_float2(c.y, d.y), f), r[k]);
         }
         Tin *dx = static_cast<Tin *>(p.dx) + first;
+        const auto to_dx = [&](auto all) {
+            Tin *to = dx;
 #pragma unroll
         for (int q = 0; q < G::kPairs; q += kRun) {
             const int i = G::chan(q);
-            const bool second = V == 1 && i + 1 < have;
-            const float2 w = param<V>(p.weight, i < have ? wc + i * G::kLc : min(c0, p.dim - 1), second, 1.f);
+            const bool second = V == 1 && (all.value || i + 1 < have);
+            const float2 w = param<V>(p.weight, all.value || i < have ? wc + i * G::kLc : min(c0, p.dim - 1), second, 1.f);
             float2 v[kRun], sum = both(0.f);
 #pragma unroll
             for (int k = 0; k < kRun; ++k) {
@@ -795,10 +808,14 @@ __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 2 : 1) norm_steps_bwd
                 sum = add2(sum, gv);
                 v[k] = fma2(add2(x.pair(q + k), nm[k]), s2[k], fma2(mul2(gv, w), r[k], s1[k]));
             }
-            if (i < have && at.in) store_pairs<V>(dx + i * apart, apart, v, second);
+            if ((all.value || i < have) && at.in) store_pairs<V>(to, apart, v, second);
+            to += (V == 1 ? 2 : (q + kRun) % G::kStats ? 0 : 1) * apart;
             if constexpr (V == 1) term[i] = sum.x, term[i + 1] = sum.y;
             else term[i] = sum.x + sum.y;
         }
+        };
+        if (have == G::kN) to_dx(std::true_type{});
+        else to_dx(std::false_type{});
         if (p.sums) db += lane_sums<G::kN>(term, lane);
     }
     if (p.sums && sl < have) {
@@ -819,7 +836,7 @@ __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 2 : 1) norm_steps_bwd
 // one shuffle at the end.  32 words so cover 63 steps of both kinds; tiles do
 // not cross batch entries, where a word's two steps are not neighbours.
 // (8 x 1536 x 2047: 53 us, 64 in single steps; fp32 3 x 1000 x 4099 took 41
-// against 35, and the backward, whose words fill the registers, 98 against 96:
+// against 35, and the backward, whose words fill the registers, 98 against 80:
 // those stay with single steps.)
 constexpr int kPairSteps = 63, kPairWarps = 8;
 using Half = __nv_bfloat16;
@@ -1551,8 +1568,8 @@ NormPlan norm_plan(const ss_desc *desc, NormWords words, bool back) {
         return pl;
     }
     // The channels in the registers of up to 8 blocks of 8 warps, or of 16
-    // where 8 do not hold them (8 x 1536 x 2047 bf16 with blocks of 16: forward
-    // 90 us against 64, backward 98 against 96).
+    // where 8 do not hold them (8 x 1536 x 2047 bf16, forward in single steps:
+    // 90 us with blocks of 16, 64 with 8).
     pl.max_warps = need <= 64 ? 8 : 16;
     const int64_t nblk = (need + pl.max_warps - 1) / pl.max_warps;
     if (nblk <= 8) {
