@@ -518,8 +518,8 @@ ss_status ss_fwd_hostio_streams(const ss_desc *desc, const void *h_u, const void
  *   y       device, (B, D, L) out_dtype
  *   mean, rstd  device, (B, L) float32 outputs, or NULL: m and r, for
  *           ss_norm_bwd (mean is not written with rms)
- * An empty tensor launches nothing.  SS_ERR_BAD_SHAPE for dim >= 2^31, more
- * than 2^31 rows (L = 1) or 2^32 steps (batch * L).
+ * An empty tensor launches nothing.  SS_ERR_BAD_SHAPE from dim = 2^31, 2^31
+ * rows (L = 1) or 2^32 - 1 steps (batch * L) on.
  */
 ss_status ss_norm_fwd(const ss_desc *desc, const void *x, const float *weight, const float *bias, float eps, int rms,
                       void *y, float *mean, float *rstd, ss_stream_t stream);
@@ -564,7 +564,7 @@ size_t ss_norm_bwd_workspace_bytes(const ss_desc *desc);
  *           of the next piece
  * x is read where its neighbours' outputs are written, so y == x, and
  * last_state == initial_state (L > 0), are refused with SS_ERR_OVERLAP.
- * SS_ERR_BAD_SHAPE for another width.
+ * SS_ERR_BAD_SHAPE for another width, and from 2^28 rows (batch * dim) on.
  */
 ss_status ss_conv_fwd(const ss_desc *desc, int width, const void *x, const float *weight, const float *bias, int silu,
                       const void *initial_state, const uint8_t *reset, void *y, void *last_state, ss_stream_t stream);
@@ -606,8 +606,8 @@ ss_status ss_conv_step(const ss_desc *desc, int width, const void *x, const floa
  *   last_state  device, (B, D) float32 output, or NULL
  *   ckpt     device, ss_glr_ckpt_elems(desc) float32 output, or NULL: states
  *            along the rows for ss_glr_bwd
- * With L = 0 the last state is the initial one.  SS_ERR_BAD_SHAPE for more
- * than 2^31 rows (batch * dim).
+ * With L = 0 the last state is the initial one.  SS_ERR_BAD_SHAPE from 2^31
+ * rows (batch * dim) on.
  */
 ss_status ss_glr_fwd(const ss_desc *desc, const void *x, const void *g, const void *z, int gate_sigmoid, int couple,
                      const float *initial_state, const uint8_t *reset, void *y, float *last_state, float *ckpt,

@@ -165,3 +165,12 @@ W4 = torch.zeros(6, 4)
 def test_binding_refuses(lib, call):
     with pytest.raises(ValueError):
         call()
+
+
+@pytest.mark.parametrize("call,sizes", [(norm, (1, 1 << 31, 1)), (norm, (1 << 31, 1, 1)), (norm, (1 << 16, 1, 1 << 16)),
+                                        (norm_bwd, (1 << 16, 1, 1 << 16)), (conv, (1 << 14, 1 << 14, 5)),
+                                        (conv_bwd, (1 << 14, 1 << 14, 5)), (conv_step, (1 << 14, 1 << 14, 1)),
+                                        (glr, (1 << 16, 1 << 15, 5)), (glr_bwd, (1 << 16, 1 << 15, 5)),
+                                        (glr_step, (1 << 16, 1 << 15, 1))])
+def test_sizes_that_launches_cannot_count(lib, call, sizes):
+    assert call(lib, desc(batch=sizes[0], dim=sizes[1], seqlen=sizes[2])) == 2
