@@ -373,13 +373,19 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
     Span s, next = place((behind - 1) * blockDim.x + t, next_b);
     if (first < behind) {
         fill(next, 0);
-        // What later rounds leave for the last thread, for the first of them.
+        // What later rounds leave for the last thread, for the first of them:
+        // steps behind the row's end have a slope of zero here as there.
         if (t == (int)blockDim.x - 1 && next.tail > kSpan) {
             const int64_t row = next_b * p.dim + d;
-            for (int k = 0; k < W - 1 && k < next.tail - kSpan; ++k) {
+#pragma unroll 1
+            for (int k = 0; k < W - 1; ++k) {
                 const int64_t at = next.t0 + kSpan + k;
-                const float dyt = load_elem(dy, row * L + at);
-                heads[1][k][0] = silu ? conv_slope(both(conv_at<Tin, W>(p, row, at, w, bias)), both(dyt)).x : dyt;
+                float q = 0.f;
+                if (k < next.tail - kSpan) {
+                    q = load_elem(dy, row * L + at);
+                    if (silu) q = conv_slope(both(conv_at<Tin, W>(p, row, at, w, bias)), both(q)).x;
+                }
+                heads[1][k][0] = q;
             }
         }
     }

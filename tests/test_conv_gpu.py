@@ -171,3 +171,22 @@ def test_autograd():
 def test_blocks_of_a_channel(B, D, L, W, silu, every, dtype):
     """Few channels: several blocks to each, whose parts of a row meet."""
     run(B, D, L, W, dtype, silu=silu, every=every, seed=W)
+
+
+def leave_nan_behind(W, silu, every, dtype):
+    """A backward over NaN gradients in every block that the GPU holds at once:
+    what it kept in shared memory, later kernels find there."""
+    B, D, L = 1, 1200, 5000
+    x, w, dy = rand(B, D, L, dtype=dtype).cuda(), rand(D, W).cuda(), torch.full((B, D, L), float("nan"), dtype=dtype).cuda()
+    ss.causal_conv_bwd(x, w, dy, silu=silu, reset=cuda(starts(B, L, every)))
+
+
+@pytest.mark.parametrize("silu,every,dtype", [(True, 0, BF), (False, 0, F32), (True, 300, F32)])
+@pytest.mark.parametrize("B,D,L,W", [(1, 8, 2049, 4), (1, 8, 2050, 4), (1, 8, 2051, 4), (1, 8, 4097, 4), (1, 8, 4099, 4),
+                                     (1, 8, 2049, 8), (1, 8, 2052, 8), (1, 8, 2055, 8), (1, 8, 4101, 8), (1, 3, 8193, 3),
+                                     (4, 160, 674, 7), (3, 56, 2051, 7), (2, 8, 2049, 5)])
+def test_row_that_ends_just_behind_a_block(B, D, L, W, silu, every, dtype):
+    """A channel's blocks meet fewer than W - 1 steps before a row's end: the
+    steps behind the end give the block before nothing."""
+    leave_nan_behind(W, silu, every, dtype)
+    run(B, D, L, W, dtype, silu=silu, every=every, seed=L + W)
