@@ -190,3 +190,48 @@ def test_row_that_ends_just_behind_a_block(B, D, L, W, silu, every, dtype):
     steps behind the end give the block before nothing."""
     leave_nan_behind(W, silu, every, dtype)
     run(B, D, L, W, dtype, silu=silu, every=every, seed=L + W)
+
+
+def against_reference(x, w, b, silu, dy, h0, reset, dl, what):
+    """Forward and backward against the 64-bit values, non-finite ones included."""
+    y, last = ss.causal_conv_fwd(cuda(x), cuda(w), cuda(b), silu=silu, initial_state=cuda(h0), reset=cuda(reset),
+                                 return_last_state=True)
+    v, e = R.conv_fwd(d64(x), d64(w), d64(b), silu, d64(h0), reset)
+    R.check(y, v["y"], e["y"], what + " y"), R.check(last, v["last"], e["last"], what + " last state")
+    g = ss.causal_conv_bwd(cuda(x), cuda(w), cuda(dy), bias=cuda(b), silu=silu, initial_state=cuda(h0),
+                           reset=cuda(reset), d_last_state=cuda(dl))
+    v, e = R.conv_bwd(d64(x), d64(w), d64(b), silu, d64(dy), d64(h0), reset, d64(dl))
+    for k in ("dx", "dweight", "dbias", "dinitial_state"):
+        if g[k] is not None:
+            R.check(g[k], v[k], e[k], f"{what} {k}")
+    return g
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("W,silu,dtype", [(2, True, F32), (4, True, BF), (4, False, F32), (8, True, F32), (8, False, BF)])
+@pytest.mark.parametrize("L", [1, 5, 37, 64, 301, 2049])
+def test_nonfinite_state_behind_a_start(L, W, silu, dtype, value):
+    """A row whose first step is a start uses no state: whatever the state
+    holds, no gradient of a weight, the bias or another row knows of it, on
+    the 8-element grid or off it."""
+    B, D = 3, 5
+    x, w, b = rand(B, D, L, seed=1, dtype=dtype), rand(D, W, seed=2), rand(D, seed=3)
+    dy, h0, dl = rand(B, D, L, seed=4, dtype=dtype), rand(B, D, W - 1, seed=5, dtype=dtype), rand(B, D, W - 1, seed=6, dtype=dtype)
+    reset = starts(B, L, 40, seed=7)
+    reset[0, 0], reset[1, 0], reset[2, 0] = 1, 0, 1
+    h0[0], h0[2] = value, value
+    g = against_reference(x, w, b, silu, dy, h0, reset, dl, f"{B}x{D}x{L} width {W} {dtype}")
+    assert all(bool(torch.isfinite(v).all()) for v in g.values())
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("W,silu,dtype", [(2, False, F32), (4, False, BF), (4, True, F32), (8, False, F32), (8, True, BF)])
+@pytest.mark.parametrize("L,every", [(3, 0), (37, 0), (40, 0), (40, 9), (301, 50), (2049, 0)])
+def test_nonfinite_at_a_row_end(L, every, W, silu, dtype, value):
+    """An infinity or a NaN among the last inputs, or in the state of a row that
+    goes on from it, reaches those weights' gradients that have a part in it."""
+    B, D = 3, 5
+    x, w, b = rand(B, D, L, seed=1, dtype=dtype), rand(D, W, seed=2), rand(D, seed=3)
+    dy, h0 = rand(B, D, L, seed=4, dtype=dtype), rand(B, D, W - 1, seed=5, dtype=dtype)
+    x[1, 0, L - 1], x[2, 1, max(L - 2, 0)], x[0, 2, max(L - W, 0)], h0[1, 3, W - 2] = (value,) * 4
+    against_reference(x, w, b, silu, dy, h0, starts(B, L, every), None, f"{B}x{D}x{L} width {W} {dtype}")
