@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvParams p) {
     for (int j = 1; j < kMaxWidth; ++j)
         if (j == W - 1) acc = fmaf(wv[j], xv, acc);
     put(state, W - 2, xv);
-    put(static_cast<Tout *>(p.y), row, p.silu ? silu2(both(acc)).x : acc);
+    put(static_cast<Tout *>(p.y), row, p.silu ? silu2<Tin>(both(acc)).x : acc);
 }
 
 template <typename Tin, typename Tout>

@@ -98,7 +98,8 @@ __device__ __forceinline__ float conv_at(const ConvParams &p, int64_t row, int64
 }
 
 // dy silu'(p).
-__device__ __forceinline__ float2 conv_slope(float2 pre, float2 dy) { return mul2(dy, silu_slope2(pre, sigmoid2(pre))); }
+template <typename T>
+__device__ __forceinline__ float2 conv_slope(float2 pre, float2 dy) { return mul2(dy, silu_slope2(pre, sigmoid2<T>(pre))); }
 
 constexpr int kSpan = 16;  // steps of a thread
 
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(const ConvParams p) {
     }
     if (p.silu) {
 #pragma unroll
-        for (int i = 0; i < kV; ++i) out[i] = silu2(out[i]);
+        for (int i = 0; i < kV; ++i) out[i] = silu2<Tin>(out[i]);
     }
     float y0[kV], y1[kV];
 #pragma unroll
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
                 float q = 0.f;
                 if (k < next.tail - kSpan) {
                     q = load_elem(dy, row * L + at);
-                    if (silu) q = conv_slope(both(conv_at<Tin, W>(p, row, at, w, bias)), both(q)).x;
+                    if (silu) q = conv_slope<Tin>(both(conv_at<Tin, W>(p, row, at, w, bias)), both(q)).x;
                 }
                 heads[1][k][0] = q;
             }
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
                 float2 pre = both(bias);
 #pragma unroll
                 for (int j = 0; j < W; ++j) pre = fma2(both(w[j]), tap[j], pre);
-                slope[k] = conv_slope(pre, slope[k]);
+                slope[k] = conv_slope<Tin>(pre, slope[k]);
             }
 #pragma unroll
             for (int j = 0; j < W; ++j) sum2[j] = fma2(slope[k], tap[j], sum2[j]);
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
             for (int k = max(-s.head, 0); k < min(s.tail, kSpan); ++k) {
                 const int64_t row = b * p.dim + d, at = s.t0 + k;
                 float q = load_elem(dy, row * L + at);
-                if (silu) q = conv_slope(both(conv_at<Tin, W>(p, row, at, w, bias)), both(q)).x;
+                if (silu) q = conv_slope<Tin>(both(conv_at<Tin, W>(p, row, at, w, bias)), both(q)).x;
                 bool seen = true;
 #pragma unroll
                 for (int j = W - 1; j >= 0; --j) {  // from step `at` back
@@ -568,7 +569,7 @@ __global__ void __launch_bounds__(kConvBwdThreads, 4) conv_bwd_kernel(const Conv
                 if (!seen) break;
                 const float pre = silu ? conv_at<Tin, W>(p, row, t, w, bias) : 0.f;
                 const float dyt = load_elem(dy, row * L + t);
-                const float slope = silu ? conv_slope(both(pre), both(dyt)).x : dyt;
+                const float slope = silu ? conv_slope<Tin>(both(pre), both(dyt)).x : dyt;
 #pragma unroll
                 for (int j = 0; j < W; ++j)
                     if (j == k - t) acc = fmaf(w[j], slope, acc);

@@ -73,20 +73,20 @@ __device__ __forceinline__ void with_flags(bool sigmoid, bool couple, F f) {
     }
 }
 
-// a, 1 - a of two gate inputs.  e = exp(-g) has its exponent held below
-// 2^126 (a NaN passes), so 1 / (1 + e) and e / (1 + e) are both finite, and
-// each has its full relative precision: 1 - a of a slow decay does not come
-// from a subtraction.
+// a, 1 - a of two gate inputs.  With g held from -87 on (a NaN passes),
+// e = exp(-g) stays below 2^126, so 1 / (1 + e) and e / (1 + e) are finite and
+// not flushed, and each has its full relative precision: 1 - a of a slow decay
+// does not come from a subtraction.  (The least a is some 10^-38.)
+template <typename T>
 __device__ __forceinline__ void gate2(float2 g, bool sigmoid, float2 &a, float2 &keep) {
     if (!sigmoid) {
         a = g;
         keep = sub2(both(1.f), g);
     } else {
-        float2 t = mul2(g, both(-kLog2e));
-        asm("min.NaN.f32 %0, %1, %2;" : "=f"(t.x) : "f"(t.x), "f"(126.f));
-        asm("min.NaN.f32 %0, %1, %2;" : "=f"(t.y) : "f"(t.y), "f"(126.f));
-        const float2 e = make_float2(sfu_exp2(t.x), sfu_exp2(t.y)), u = add2(e, both(1.f));
-        a = make_float2(sfu_rcp(u.x), sfu_rcp(u.y));
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(g.x) : "f"(g.x), "f"(-87.f));
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(g.y) : "f"(g.y), "f"(-87.f));
+        const float2 e = exp_neg2<T>(g);
+        a = rcp2(add2(e, both(1.f)));
         keep = mul2(e, a);
     }
 }
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(512) glr_fwd_kernel(const GlrParams p, int lan
 #pragma unroll
             for (int i = 0; i < kE; i += 2) {
                 float2 a2, k2, b2 = nx[i / kV].pair(i % kV / 2);
-                gate2(ng[i / kV].pair(i % kV / 2), sig.value, a2, k2);
+                gate2<Tin>(ng[i / kV].pair(i % kV / 2), sig.value, a2, k2);
                 if (cpl.value) b2 = mul2(k2, b2);
                 a[i] = a2.x, a[i + 1] = a2.y, b[i] = b2.x, b[i + 1] = b2.y;
             }
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(512) glr_fwd_kernel(const GlrParams p, int lan
 #pragma unroll
             for (int i = 0; i < kV; i += 2) {
                 float2 h2 = make_float2(b[k * kV + i], b[k * kV + i + 1]);
-                if constexpr (kZ) h2 = mul2(h2, silu2(cz[k].pair(i / 2)));
+                if constexpr (kZ) h2 = mul2(h2, silu2<Tin>(cz[k].pair(i / 2)));
                 o[i] = h2.x, o[i + 1] = h2.y;
             }
             if (inner && vec) {
@@ -383,10 +383,10 @@ __global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p, int lan
         float2 a[kV / 2], keep[kV / 2];
         if (sigmoid) {
 #pragma unroll
-            for (int i = 0; i < kV / 2; ++i) gate2(ng.pair(i), true, a[i], keep[i]);
+            for (int i = 0; i < kV / 2; ++i) gate2<Tin>(ng.pair(i), true, a[i], keep[i]);
         } else {
 #pragma unroll
-            for (int i = 0; i < kV / 2; ++i) gate2(ng.pair(i), false, a[i], keep[i]);
+            for (int i = 0; i < kV / 2; ++i) gate2<Tin>(ng.pair(i), false, a[i], keep[i]);
         }
         if (!inner) {
             int lo, hi;
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(512) glr_bwd_kernel(const GlrParams p, int lan
             if constexpr (kZ) {
                 // dy silu(z) and dy silu'(z)
                 const float2 zv = nz.pair(i);
-                const float2 s = sigmoid2(zv);
+                const float2 s = sigmoid2<Tin>(zv);
                 dzv[i] = mul2(dh[i], silu_slope2(zv, s));
                 dh[i] = mul2(dh[i], mul2(s, zv));
             }
@@ -516,14 +516,14 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const GlrParams p) {
     const int64_t row = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (row >= p.rows) return;
     float2 a2, keep2;
-    gate2(both(load_elem(static_cast<const Tin *>(p.g), row)), p.sigmoid, a2, keep2);
+    gate2<Tin>(both(load_elem(static_cast<const Tin *>(p.g), row)), p.sigmoid, a2, keep2);
     const float a = a2.x, keep = keep2.x;
     const float xv = load_elem(static_cast<const Tin *>(p.x), row);
     const float h = fmaf(a, p.last[row], p.couple ? keep * xv : xv);
     p.last[row] = h;
     float yv = h;
     if (p.z) {
-        yv *= silu2(both(load_elem(static_cast<const Tin *>(p.z), row))).x;
+        yv *= silu2<Tin>(both(load_elem(static_cast<const Tin *>(p.z), row))).x;
     }
     put(static_cast<Tout *>(p.y), row, yv);
 }

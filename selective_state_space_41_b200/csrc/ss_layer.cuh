@@ -141,16 +141,27 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 __device__ __forceinline__ int clamp8(int64_t v) { return v < 0 ? 0 : v > kV ? kV : (int)v; }
 
-// 1 / (1 + exp(-v)) of two values: exponential (2 ulp) and reciprocal (1 ulp)
-// on the SFU, some 4 10^-7 relative at most beyond the rounding of the
-// exponent's argument, for fp32 inputs too (with expf and an IEEE division the
-// fp32 convolution's backward took 91 us instead of 80, 4 x 1024 x 4096).  exp(-v) may overflow, to
-// a result of zero.
-__device__ __forceinline__ float2 sigmoid2(float2 v) {
-    const float2 t = mul2(v, both(-kLog2e)), u = add2(make_float2(sfu_exp2(t.x), sfu_exp2(t.y)), both(1.f));
-    return make_float2(sfu_rcp(u.x), sfu_rcp(u.y));
+// exp(-v) of two values that go into results of inputs of type T.  bf16
+// inputs, whose values carry 2^-9: on the SFU (2 ulp), beyond which the
+// rounding of v log2 e adds |v| 2^-24.  fp32 inputs: expf, whose error does not
+// grow with |v|.  (fp32 with 2^x on the SFU: 10^-6 relative at v = -20 where
+// this has 2.7 10^-7; 4 x 1024 x 4096 convolution 27.0 us, backward 61.9, with
+// expf 28.8 and 63.6; recurrence forward and backward with the gate 121.2, 122.7.)
+template <typename T>
+__device__ __forceinline__ float2 exp_neg2(float2 v) {
+    if constexpr (sizeof(T) == 4) return make_float2(expf(-v.x), expf(-v.y));
+    const float2 t = mul2(v, both(-kLog2e));
+    return make_float2(sfu_exp2(t.x), sfu_exp2(t.y));
 }
-__device__ __forceinline__ float2 silu2(float2 v) { return mul2(v, sigmoid2(v)); }
+// The reciprocal on the SFU (1 ulp) for both types: an IEEE division takes
+// those fp32 cases to 69.1 and 140.4 us, and the error from 2.2 to 2.0 10^-7
+// for |v| <= 1.
+__device__ __forceinline__ float2 rcp2(float2 u) { return make_float2(sfu_rcp(u.x), sfu_rcp(u.y)); }
+// 1 / (1 + exp(-v)).  exp(-v) may overflow, to a result of zero.
+template <typename T>
+__device__ __forceinline__ float2 sigmoid2(float2 v) { return rcp2(add2(exp_neg2<T>(v), both(1.f))); }
+template <typename T>
+__device__ __forceinline__ float2 silu2(float2 v) { return mul2(v, sigmoid2<T>(v)); }
 // silu'(v) = s (1 + v (1 - s)), given s = sigmoid(v).
 __device__ __forceinline__ float2 silu_slope2(float2 v, float2 s) { return mul2(s, fma2(v, sub2(both(1.f), s), both(1.f))); }
 

@@ -333,3 +333,41 @@ def test_more_than_2_31_elements():
     gt = ss.layer_norm_bwd(x[..., -40:].contiguous(), y[..., -40:].contiguous(), rstd[:, -40:].contiguous(),
                            mean[:, -40:].contiguous(), b)["dx"]
     assert float((g[..., -40:].float() - gt.float()).abs().max()) <= 2.0 ** -7 * float(gt.float().abs().max())
+
+
+@pytest.mark.parametrize("lo,hi", [(-1, 1), (-5, 5), (-20, -5), (5, 20), (-80, -20)])
+def test_logistic_function_of_fp32(lo, hi):
+    """silu of the convolution, the recurrence's decay, its complement and its
+    output gate keep their relative precision however large the argument.
+
+    Tolerances, in units of U = 2^-24: the exponential 4 (2 ulp), the sum 1, the
+    reciprocal 2 (1 ulp), a product 1: 8 for silu and the complement (in which
+    the exponential's error counts once, as the sum's share of it falls out);
+    with the gate's product and a state of one 9.  silu' = s (1 + v (1 - s)) for
+    v <= -5: s 7, the bracket 3 (its part v (1 - s) is at most 5/4 of it), two
+    products."""
+    n = 250_000
+    v = torch.linspace(lo, hi, n, dtype=torch.float64).float().cuda()
+    d = v.double()
+    s, k = 1 / (1 + torch.exp(-d)), 1 / (1 + torch.exp(d))
+
+    def near(got, want, units, what):
+        off = float(((got.flatten().double() - want).abs() / want.abs()).nan_to_num(0.0).max()) / R.U
+        assert off <= units, f"{what}: {off:.1f} units"
+
+    row, w = v.view(1, 1, n), torch.tensor([[0.0, 1.0]], device="cuda")
+    one, state = torch.ones(n // 500, 500, 1, device="cuda"), torch.ones(n // 500, 500, device="cuda")
+    g = v.view(one.shape)
+    near(ss.causal_conv_fwd(row, w, silu=True), d * s, 8, "silu")
+    near(ss.gated_recurrence_fwd(0 * one, g, initial_state=state), s, 8, "decay")
+    near(ss.gated_recurrence_fwd(one, g, couple=True), k, 8, "complement")
+    near(ss.gated_recurrence_fwd(one, 0 * one, g, gate_sigmoid=False), d * s, 9, "output gate")
+    near(ss.gated_recurrence_step(0 * state, g[..., 0], state), s, 8, "decay of a step")
+    y = ss.causal_conv_step(g[..., 0], w.expand(500, 2), 0 * one, silu=True)
+    near(y, d * s, 8, "silu of a step")
+    if hi <= -5:
+        dx = ss.causal_conv_bwd(row, w, torch.ones_like(row), silu=True)["dx"]
+        near(dx, s * (1 + d * k), 12, "silu'")
+        ck = ss.gated_recurrence_fwd(one, 0 * one, g, gate_sigmoid=False, return_ckpt=True)[1]
+        dz = ss.gated_recurrence_bwd(one, 0 * one, one, ck, g, gate_sigmoid=False)["dz"]
+        near(dz, s * (1 + d * k), 12, "gradient of the output gate")
