@@ -596,7 +596,10 @@ ss_status ss_conv_step(const ss_desc *desc, int width, const void *x, const floa
  *   a[b,d,t] = g[b,d,t], or sigmoid(g[b,d,t])   (gate_sigmoid != 0)
  *   h[b,d] <- a h[b,d] + x[b,d,t],  or  a h + (1 - a) x   (couple != 0)
  *   y[b,d,t] = h[b,d], times silu(z[b,d,t]) when z is given
- *   x, g, z  device, (B, D, L) in_dtype (z NULL: no output gate)
+ *   x, g, z  device, (B, D, L) in_dtype (z NULL: no output gate).  Without
+ *            gate_sigmoid, g must lie in [-1, 1]: products of up to 512 decays
+ *            are formed before they meet a state, and where larger ones
+ *            overflow, results are NaN even if the state is zero
  *   initial_state  device, (B, D) float32: the state before step 0, or NULL
  *            (zero); may be the same buffer as last_state
  *   reset    device, (B, L) bytes, or NULL: nonzero where a new sequence

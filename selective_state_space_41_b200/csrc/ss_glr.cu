@@ -24,6 +24,11 @@
 // are issued before the current ones are worked on; gates and products are
 // computed in pairs of steps with the packed arithmetic of two floats.
 //
+// The A of a map is a product of up to 512 decays.  With decays of at most one
+// in size it cannot overflow, and an A that underflows to zero loses no more
+// than the state's own decay does; larger ones are outside the operator's
+// domain (an infinite A and a state of zero give NaN).
+//
 // Sequence starts cut the maps: behind a start the entering state does not
 // count, whatever it is (an infinity or a NaN of another sequence included),
 // so a cut is carried as a bit and selects instead of multiplying by zero.

@@ -412,7 +412,8 @@ def ss_glr_fwd(x, g, y, z=None, gate_sigmoid=True, couple=False, initial_state=N
     only the states are wanted).  z: output gate; initial_state, last_state:
     (batch, dim) float32, one buffer or two; reset: (batch, L) uint8 or bool,
     nonzero where a sequence starts; ckpt: ss_glr_ckpt_elems() float32, for
-    the backward."""
+    the backward.  g is a decay's logit, or with ``gate_sigmoid`` false the
+    decay, in [-1, 1] (products of larger ones may overflow, to NaN)."""
     x = _main(x, (3,), "x")
     out = x.dtype if y is None else _out_type(y.dtype, x, "y")
     _output(y, "y", x.shape, out, x), _output(last_state, "last_state", x.shape[:2], _F32, x)
@@ -426,7 +427,8 @@ def ss_glr_fwd(x, g, y, z=None, gate_sigmoid=True, couple=False, initial_state=N
 def gated_recurrence_fwd(x, g, z=None, gate_sigmoid=True, couple=False, initial_state=None, reset=None,
                          return_last_state=False, return_ckpt=False, out_dtype=None):
     """y of the gated linear recurrence, then the last state
-    (``return_last_state``) and the backward's checkpoints (``return_ckpt``)."""
+    (``return_last_state``) and the backward's checkpoints (``return_ckpt``).
+    g: the decays' logits, or with ``gate_sigmoid`` false decays in [-1, 1]."""
     x = _main(x, (3,), "x")
     out = _out_type(out_dtype or x.dtype, x, "out_dtype")
     y, desc = _new(x, out), _desc(*x.shape, x, out)
@@ -529,5 +531,6 @@ class GatedRecurrenceFn(torch.autograd.Function):
 def gated_recurrence_fn(x, g, z=None, gate_sigmoid=True, couple=False, initial_state=None, reset=None,
                         return_last_state=False):
     """y (and the float32 last state) of the gated linear recurrence,
-    differentiable; see GatedRecurrenceFn."""
+    differentiable; see GatedRecurrenceFn.  g: the decays' logits, or with
+    ``gate_sigmoid`` false decays in [-1, 1]."""
     return GatedRecurrenceFn.apply(x, g, z, initial_state, reset, gate_sigmoid, couple, return_last_state)

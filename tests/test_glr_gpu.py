@@ -227,3 +227,31 @@ def test_same_bits_over_several_blocks():
     d = ss.gated_recurrence_bwd(x, g, x, ck)
     df = ss.gated_recurrence_bwd(*few, few[0], ckf)
     assert torch.equal(d["dx"][:, :16], df["dx"]) and torch.equal(d["dg"][:, :16], df["dg"])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("couple", [True, False])
+@pytest.mark.parametrize("B,D,L", [(1, 3, 700), (2, 40, 45), (1, 2, 25001)])
+def test_decays_over_their_whole_range(B, D, L, couple, dtype):
+    """Decays of either sign up to one in size, runs of zeros, of ones and of
+    decays whose products vanish, beside inputs and states of zero."""
+    g = rand(B, D, L, seed=L).clamp(-1, 1)
+    g[..., L // 5:L // 4] = 0
+    g[..., L // 4:L // 3] = 1e-6
+    g[..., L // 3:L // 2] = -1
+    g[..., L // 2:2 * L // 3] = 1
+    x = rand(B, D, L, seed=L + 1)
+    x[..., L // 4:2 * L // 3] = 0
+    x, g = x.to(dtype), g.to(dtype)
+    what = f"{B}x{D}x{L} {dtype}"
+    dy = rand(B, D, L, seed=L + 2, dtype=dtype)
+    for h0 in (None, rand(B, D, seed=L + 3)):
+        y, last, ck = ss.gated_recurrence_fwd(x.cuda(), g.cuda(), gate_sigmoid=False, couple=couple, initial_state=cuda(h0),
+                                              return_last_state=True, return_ckpt=True)
+        v, e = R.glr_fwd(d64(x), d64(g), None, False, couple, d64(h0))
+        R.check(y, v["y"], e["y"], what + " y"), R.check(last, v["last"], e["last"], what + " last state")
+        d = ss.gated_recurrence_bwd(x.cuda(), g.cuda(), dy.cuda(), ck, gate_sigmoid=False, couple=couple,
+                                    return_dinitial_state=True)
+        v, e = R.glr_bwd(d64(x), d64(g), d64(dy), None, False, couple, d64(h0))
+        for k in ("dx", "dg", "dinitial_state"):
+            R.check(d[k], v[k], e[k], f"{what} {k}")
