@@ -688,6 +688,8 @@ __device__ __forceinline__ float lane_sums(float (&v)[kN], int lane) {
 // fp32: 55 us with the second kernel's 5 or so, against 22.5 for the bytes:
 // 16 warps an SM and a cluster barrier for each 32 steps (issue 45 %).  8 x
 // 1536 x 2047 bf16: 80 us (95 where full warps too ask which channels there are).
+// bf16 x with fp32 dy: 82 us there; in vectors, where a lane's registers spill,
+// 95 us for 8 x 1536 x 2048.
 template <typename Tin, typename Tout, int V, int kMaxW>
 __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 2 : 1) norm_steps_bwd_kernel(const NormParams p, int nblk) {
     using G = Tile<V>;
@@ -728,21 +730,21 @@ __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 2 : 1) norm_steps_bwd
         // (all: every channel of the thread is there)
         const auto to_sums = [&](auto all) {
 #pragma unroll
-        for (int q = 0; q < G::kPairs; q += kRun) {
-            const int i = G::chan(q);
-            const bool second = V == 1 && (all.value || i + 1 < have);
-            const float2 w = param<V>(p.weight, all.value || i < have ? wc + i * G::kLc : min(c0, p.dim - 1), second, 1.f);
-            float2 sum = both(0.f);
+            for (int q = 0; q < G::kPairs; q += kRun) {
+                const int i = G::chan(q);
+                const bool second = V == 1 && (all.value || i + 1 < have);
+                const float2 w = param<V>(p.weight, all.value || i < have ? wc + i * G::kLc : min(c0, p.dim - 1), second, 1.f);
+                float2 sum = both(0.f);
 #pragma unroll
-            for (int k = 0; k < kRun; ++k) {
-                const float2 gv = g.pair(q + k), t = mul2(gv, mul2(add2(x.pair(q + k), nm[k]), r[k]));
-                s1[k] = fma2(gv, w, s1[k]);
-                s2[k] = fma2(t, w, s2[k]);
-                sum = add2(sum, t);
+                for (int k = 0; k < kRun; ++k) {
+                    const float2 gv = g.pair(q + k), t = mul2(gv, mul2(add2(x.pair(q + k), nm[k]), r[k]));
+                    s1[k] = fma2(gv, w, s1[k]);
+                    s2[k] = fma2(t, w, s2[k]);
+                    sum = add2(sum, t);
+                }
+                if constexpr (V == 1) term[i] = sum.x, term[i + 1] = sum.y;
+                else term[i] = sum.x + sum.y;
             }
-            if constexpr (V == 1) term[i] = sum.x, term[i + 1] = sum.y;
-            else term[i] = sum.x + sum.y;
-        }
         };
         if (have == G::kN) to_sums(std::true_type{});
         else to_sums(std::false_type{});
@@ -797,22 +799,22 @@ __global__ void __launch_bounds__(32 * kMaxW, kMaxW <= 8 ? 2 : 1) norm_steps_bwd
         const auto to_dx = [&](auto all) {
             Tin *to = dx;
 #pragma unroll
-        for (int q = 0; q < G::kPairs; q += kRun) {
-            const int i = G::chan(q);
-            const bool second = V == 1 && (all.value || i + 1 < have);
-            const float2 w = param<V>(p.weight, all.value || i < have ? wc + i * G::kLc : min(c0, p.dim - 1), second, 1.f);
-            float2 v[kRun], sum = both(0.f);
+            for (int q = 0; q < G::kPairs; q += kRun) {
+                const int i = G::chan(q);
+                const bool second = V == 1 && (all.value || i + 1 < have);
+                const float2 w = param<V>(p.weight, all.value || i < have ? wc + i * G::kLc : min(c0, p.dim - 1), second, 1.f);
+                float2 v[kRun], sum = both(0.f);
 #pragma unroll
-            for (int k = 0; k < kRun; ++k) {
-                const float2 gv = g.pair(q + k);
-                sum = add2(sum, gv);
-                v[k] = fma2(add2(x.pair(q + k), nm[k]), s2[k], fma2(mul2(gv, w), r[k], s1[k]));
+                for (int k = 0; k < kRun; ++k) {
+                    const float2 gv = g.pair(q + k);
+                    sum = add2(sum, gv);
+                    v[k] = fma2(add2(x.pair(q + k), nm[k]), s2[k], fma2(mul2(gv, w), r[k], s1[k]));
+                }
+                if ((all.value || i < have) && at.in) store_pairs<V>(to, apart, v, second);
+                to += (V == 1 ? 2 : (q + kRun) % G::kStats ? 0 : 1) * apart;
+                if constexpr (V == 1) term[i] = sum.x, term[i + 1] = sum.y;
+                else term[i] = sum.x + sum.y;
             }
-            if ((all.value || i < have) && at.in) store_pairs<V>(to, apart, v, second);
-            to += (V == 1 ? 2 : (q + kRun) % G::kStats ? 0 : 1) * apart;
-            if constexpr (V == 1) term[i] = sum.x, term[i + 1] = sum.y;
-            else term[i] = sum.x + sum.y;
-        }
         };
         if (have == G::kN) to_dx(std::true_type{});
         else to_dx(std::false_type{});
