@@ -15,9 +15,11 @@
 //
 // Forward: two bytes in and two out per bf16 element against 2 W + 5
 // operations.  8 x 1536 x 2048 bf16, W = 4, SiLU: 23 us (15.4 for the bytes),
-// the exponential and the reciprocal on the SFU 59 % busy and issue 65 %.  With
-// starts (2 x 1024 x 20011, W = 5, every 500): 63 us (25.0), the tests of the
-// taps and the unpacking of bf16 on the integer pipe.
+// issue 66 %, half of the warps an SM can hold, mostly waiting for loads; the
+// SFU's 60 % is not the limit (21.6 us without SiLU).  fp32, 4 x 1024 x 4096:
+// 28.8 us (20.5 for the bytes).  With starts (2 x 1024 x 20011, W = 5, every
+// 500): 62 us (25.0), the tests of the taps and the unpacking of bf16 on the
+// integer pipe.
 //
 // Backward: with q_t = dy_t (silu'(p_t)),
 //   dx_s = sum_j w_j q_(s + (W-1) - j),   dw_j = sum_t q_t x_(t - (W-1) + j),   dbias = sum_t q_t.
@@ -25,8 +27,8 @@
 // from the next thread through shared memory, and for the block's last thread
 // from the round before: a block works its spans from the last to the first
 // (each thread computing them itself: 51.9 us where this takes 47, 8 x 1536 x
-// 2048 bf16, W = 4, SiLU; 23.1 for the bytes; 16 warps an SM at 109 registers
-// issue 52 % of the time).
+// 2048 bf16, W = 4, SiLU; 23.1 for the bytes; 16 warps an SM at 110 registers
+// issue 53 % of the time; fp32 4 x 1024 x 4096 63.7, 30.7 for the bytes).
 // dw and dbias sum over batch and steps for each channel, so a block (or a
 // cluster of blocks, when the channels are few) takes one channel and all of
 // its batch entries; every thread keeps its W + 1 sums in registers over all

@@ -36,9 +36,9 @@ cudaError_t fwd(cudaStream_t s, ConvParams &p) {
 template <int W>
 cudaError_t bwd(cudaStream_t s, ConvParams &p) {
     // Blocks per channel: enough for four blocks per SM, which is what runs at
-    // once, no more than the channel's spans feed.  (fp32 4 x 1024 x 4096: 63
-    // us, 68 with eight per SM wanted and 78 with sixteen; bf16 2 x 1024 x 20011
-    // with starts 149, 172 and 201; 4 x 64 x 65536: 38 with each.)
+    // once, no more than the channel's spans feed.  (fp32 4 x 1024 x 4096: 64
+    // us, 68 with eight per SM wanted and 79 with sixteen; bf16 2 x 1024 x 20011
+    // with starts 145, 169 and 198; 4 x 64 x 65536: 38 with each.)
     const int64_t vecs = p.batch * spans_of(p.L);
     p.small = vecs <= INT_MAX;
     p.by_spans = divisor_of(spans_of(p.L));

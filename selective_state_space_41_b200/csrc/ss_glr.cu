@@ -9,9 +9,10 @@
 // and some twenty operations: the kernels are bound by memory, and close
 // behind it by the instructions they issue.  What the design has to do is to
 // keep enough loads in flight, the serial chain of the recurrence short and
-// the work per step small (4 x 1024 x 100000 bf16: 459 us, 375 for the
-// bytes; 8 x 1536 x 2048 with the output gate, forward 42 and backward 73,
-// 30.7 and 53.7 for the bytes; issue 55 to 60 %).  G lanes take a row (32, or fewer for short rows),
+// the work per step small (4 x 1024 x 100000 bf16: 460 us, 375 for the
+// bytes; 8 x 1536 x 2048 with the output gate, forward 41 and backward 73,
+// 30.7 and 53.7 for the bytes; issue 55 to 60 %; fp32 4 x 1024 x 4096 with the
+// gate, forward 47, 41.0 for the bytes).  G lanes take a row (32, or fewer for short rows),
 // 16 steps each at a time forward and 8 backward.  Each lane folds its steps
 // into one pair (A, B): the map h -> A h + B.  The pairs compose as
 // (A2, B2) o (A1, B1) = (A2 A1, A2 B1 + B2), so log2 G shuffle rounds give
